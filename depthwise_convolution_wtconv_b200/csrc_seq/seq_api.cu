@@ -1,0 +1,603 @@
+// C entries of the sequence operators (wtconv_seq.h): argument checks on the
+// host, choice of the variant, launches.
+
+#include <algorithm>
+#include <climits>
+
+#include "seq_causal.cuh"
+#include "seq_common.cuh"
+#include "seq_norm.cuh"
+#include "seq_scan.cuh"
+
+using namespace wtseq;
+
+namespace {
+
+constexpr long long MAX_ELEMENTS = 1ll << 56;  // byte offsets stay within 64 bits
+constexpr int SMS = 148;
+
+size_t elt(wtconv_dtype t) { return t == WTCONV_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+size_t rup16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+bool dtype_ok(wtconv_dtype t) { return t == WTCONV_F32 || t == WTCONV_BF16; }
+
+// Rows of an activation that the call needs.  Output rows must not overlap:
+// tokens behind one another within a batch row, or batch rows within a token.
+wtconv_status check_rows(const wtconv_rows* r, size_t e, int B, int T, long long C, bool output) {
+  if (!r || !r->data || r->batch_stride < 0 || r->token_stride < 0) return WTCONV_ERR_ARG;
+  if (r->batch_stride > MAX_ELEMENTS / B || r->token_stride > MAX_ELEMENTS / T) return WTCONV_ERR_ARG;
+  if (output) {
+    const bool by_row = (T == 1 || r->token_stride >= C) &&
+                        (B == 1 || r->batch_stride >= (long long)(T - 1) * r->token_stride + C);
+    const bool by_token = (B == 1 || r->batch_stride >= C) &&
+                          (T == 1 || r->token_stride >= (long long)(B - 1) * r->batch_stride + C);
+    if (!by_row && !by_token) return WTCONV_ERR_ARG;
+  }
+  return aligned(r->data, e) ? WTCONV_OK : WTCONV_ERR_ALIGN;
+}
+
+// A pointer that may be NULL, aligned to its elements.
+wtconv_status check_ptr(const void* p, size_t e, bool required) {
+  if (!p) return required ? WTCONV_ERR_ARG : WTCONV_OK;
+  return aligned(p, e) ? WTCONV_OK : WTCONV_ERR_ALIGN;
+}
+
+wtconv_status check_ws(const void* ws, size_t have, size_t need) {
+  if (!need) return WTCONV_OK;
+  if (!ws || have < need) return WTCONV_ERR_WORKSPACE;
+  return aligned(ws, 16) ? WTCONV_OK : WTCONV_ERR_ALIGN;
+}
+
+#define TRY(call)                                   \
+  do {                                              \
+    const wtconv_status try_status = (call);        \
+    if (try_status != WTCONV_OK) return try_status; \
+  } while (0)
+
+// Whether V channels at a time of these rows can be one access (or 16-byte
+// accesses).
+bool wide(const wtconv_rows* r, int V, size_t e, int B, int T) {
+  if (!r) return true;
+  const size_t bytes = std::min<size_t>(16, V * e);
+  return aligned(r->data, bytes) && (B == 1 || r->batch_stride * e % bytes == 0) &&
+         (T == 1 || r->token_stride * e % bytes == 0);
+}
+bool wide(const void* p, int V, size_t e) { return aligned(p, std::min<size_t>(16, V * e)); }
+
+wtconv_status launched() { return cudaGetLastError() == cudaSuccess ? WTCONV_OK : WTCONV_ERR_CUDA; }
+bool grid_ok(long long blocks) { return blocks <= INT_MAX; }
+
+// ------------------------------------------------------ causal convolution
+wtconv_status check_causal(const wtconv_causal_desc* d) {
+  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || d->k <= 0 || !dtype_ok(d->io)) return WTCONV_ERR_ARG;
+  if ((long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
+  return d->k > WTCONV_CAUSAL_MAX_K ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
+}
+
+long long causal_groups(const wtconv_causal_desc* d) {
+  return d->B * ceil_div(d->T, CAUSAL_GSTRIP * CAUSAL_GY);
+}
+size_t causal_ws(const wtconv_causal_desc* d) { return (size_t)causal_groups(d) * d->C * (d->k + 1) * sizeof(float); }
+
+template <typename IO> CausalArgs<IO> causal_args(const wtconv_causal_desc* d, const wtconv_rows* x, const float* w,
+                                                  const float* bias) {
+  CausalArgs<IO> a = {};
+  a.x = rows_of<IO>(x);
+  a.w = w;
+  a.bias = bias;
+  a.B = d->B;
+  a.T = d->T;
+  a.C = d->C;
+  a.silu = d->silu;
+  return a;
+}
+
+// Calls f with the number of taps as a compile-time constant.
+template <int V_> struct Int { static constexpr int value = V_; };
+template <typename F> wtconv_status with_taps(int k, F f) {
+  switch (k) {
+    case 1: return f(Int<1>());
+    case 2: return f(Int<2>());
+    case 3: return f(Int<3>());
+    case 4: return f(Int<4>());
+    case 5: return f(Int<5>());
+    case 6: return f(Int<6>());
+    case 7: return f(Int<7>());
+    default: return f(Int<8>());
+  }
+}
+
+template <typename IO, int V> wtconv_status causal_forward(const CausalArgs<IO>& a, int k, cudaStream_t st) {
+  const long long blocks = ceil_div((long long)(a.C / V) * a.strips * a.B, 128);
+  if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+  return with_taps(k, [&](auto K) {
+    causal_forward_kernel<IO, K.value, V><<<(unsigned)blocks, 128, 0, st>>>(a);
+    return launched();
+  });
+}
+
+template <typename IO, int V>
+wtconv_status causal_backward(const CausalArgs<IO>& a, int k, float* dw, float* dbias, cudaStream_t st) {
+  const long long groups = (long long)a.strips * a.B, blocks = ceil_div(a.C / V, 32) * groups;
+  if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+  TRY(with_taps(k, [&](auto K) {
+    causal_backward_kernel<IO, K.value, V><<<(unsigned)blocks, 256, 0, st>>>(a);
+    return launched();
+  }));
+  const long long n = (long long)a.C * (k + 1);
+  launch_sum(a.part, groups, n, n, CausalSums{dw, dbias, k}, st);
+  return launched();
+}
+
+template <typename IO, int V>
+wtconv_status causal_step(const CausalArgs<IO>& a, int k, const int* active, cudaStream_t st) {
+  const long long blocks = ceil_div((long long)(a.C / V) * a.B, 128);
+  if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+  return with_taps(k, [&](auto K) {
+    causal_step_kernel<IO, K.value, V><<<(unsigned)blocks, 128, 0, st>>>(a, active);
+    return launched();
+  });
+}
+
+// -------------------------------------------------------------------- scan
+wtconv_status check_scan(const wtconv_scan_desc* d) {
+  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || d->N <= 0 || d->G <= 0 || d->C % d->G || !dtype_ok(d->io))
+    return WTCONV_ERR_ARG;
+  if ((long long)d->B * d->T > MAX_ELEMENTS / d->C / 64) return WTCONV_ERR_ARG;
+  return d->N > WTCONV_SCAN_MAX_N ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
+}
+
+struct ScanWs {  // floats into the workspace
+  size_t ckpt, part_b, part_c, part_a, part_d, part_bias, end;
+};
+int scan_blocks(const wtconv_scan_desc* d) { return (int)ceil_div(d->C / d->G, 32); }
+ScanWs scan_backward_ws(const wtconv_scan_desc* d) {
+  ScanWs w;
+  const size_t bc = (size_t)scan_blocks(d) * d->G * d->B * d->T * d->N, tiles = ceil_div(d->T, SCAN_T);
+  w.ckpt = 0;
+  w.part_b = w.ckpt + tiles * d->B * d->N * d->C;
+  w.part_c = w.part_b + bc;
+  w.part_a = w.part_c + bc;
+  w.part_d = w.part_a + (size_t)d->B * d->C * d->N;
+  w.part_bias = w.part_d + (size_t)d->B * d->C;
+  w.end = w.part_bias + (size_t)d->B * d->C;
+  return w;
+}
+
+template <typename IO>
+ScanArgs<IO> scan_args(const wtconv_scan_desc* d, const wtconv_rows* x, const wtconv_rows* dt, const float* a,
+                       const wtconv_rows* b, const wtconv_rows* c, const float* skip, const wtconv_rows* z,
+                       const float* dt_bias) {
+  ScanArgs<IO> p = {};
+  p.x = rows_of<IO>(x);
+  p.dt = rows_of<IO>(dt);
+  p.z = rows_of<IO>(z);
+  p.b = rows_of<IO>(b);
+  p.c = rows_of<IO>(c);
+  p.a = a;
+  p.d = skip;
+  p.dt_bias = dt_bias;
+  p.B = d->B;
+  p.T = d->T;
+  p.C = d->C;
+  p.N = d->N;
+  p.G = d->G;
+  p.softplus = d->softplus;
+  p.blocks = scan_blocks(d);
+  p.tiles = (int)ceil_div(d->T, SCAN_T);
+  return p;
+}
+
+wtconv_status check_scan_inputs(const wtconv_scan_desc* d, const wtconv_rows* x, const wtconv_rows* dt, const float* a,
+                                const wtconv_rows* b, const wtconv_rows* c, const float* skip, const wtconv_rows* z,
+                                const float* dt_bias) {
+  const size_t e = elt(d->io);
+  const long long gn = (long long)d->G * d->N;
+  TRY(check_rows(x, e, d->B, d->T, d->C, false));
+  TRY(check_rows(dt, e, d->B, d->T, d->C, false));
+  TRY(check_rows(b, e, d->B, d->T, gn, false));
+  TRY(check_rows(c, e, d->B, d->T, gn, false));
+  if (z) TRY(check_rows(z, e, d->B, d->T, d->C, false));
+  TRY(check_ptr(a, 4, true));
+  TRY(check_ptr(skip, 4, false));
+  return check_ptr(dt_bias, 4, false);
+}
+
+template <typename K> wtconv_status allow_smem(K kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return WTCONV_OK;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
+             ? WTCONV_OK
+             : WTCONV_ERR_CUDA;
+}
+
+template <typename IO, bool CKPT> wtconv_status run_scan_forward(const ScanArgs<IO>& p, cudaStream_t st) {
+  const long long blocks = (long long)p.B * p.blocks * p.G;
+  if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+  const size_t smem =
+      sizeof(float) * (2 * SCAN_T * 32 + (CKPT ? 0 : SCAN_W * SCAN_T * 32) + 2 * p.N * SCAN_LD + 2 * p.N * 32);
+  TRY(allow_smem(scan_forward_kernel<IO, CKPT>, smem));
+  scan_forward_kernel<IO, CKPT><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
+  return launched();
+}
+
+// Sums of db or dc: output i = ((g * B + b) * T + t) * N + n
+template <typename IO> struct ScanRowSums {
+  Rows<IO> out;
+  int B, T, N;
+  __device__ __forceinline__ void put(long long i, float v) const {
+    const int n = (int)(i % N);
+    long long r = i / N;
+    const long long t = r % T;
+    r /= T;
+    out.at((int)(r % B), t)[r / B * N + n] = from_f<IO>(v);
+  }
+};
+
+template <typename IO>
+wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, const wtconv_rows* db, const wtconv_rows* dc,
+                                float* da, float* dd, float* ddt_bias, float* ws, cudaStream_t st) {
+  const ScanWs w = scan_backward_ws(d);
+  p.ckpt = ws + w.ckpt;
+  p.part_b = ws + w.part_b;
+  p.part_c = ws + w.part_c;
+  p.part_a = ws + w.part_a;
+  p.part_d = ws + w.part_d;
+  p.part_bias = ws + w.part_bias;
+  TRY((run_scan_forward<IO, true>(p, st)));
+  const long long blocks = (long long)p.B * p.blocks * p.G;
+  const size_t smem = sizeof(float) * (3 * SCAN_T * 32 + 3 * SCAN_W * SCAN_T * 32 + 2 * p.N * SCAN_LD + 3 * p.N * 32);
+  TRY(allow_smem(scan_backward_kernel<IO>, smem));
+  scan_backward_kernel<IO><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
+  TRY(launched());
+  const long long bc = (long long)p.G * p.B * p.T * p.N;
+  launch_sum(p.part_b, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(db), p.B, p.T, p.N}, st);
+  launch_sum(p.part_c, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(dc), p.B, p.T, p.N}, st);
+  const long long cn = (long long)p.C * p.N;
+  launch_sum(p.part_a, p.B, cn, cn, SumFloats{da}, st);
+  if (dd) launch_sum(p.part_d, p.B, p.C, p.C, SumFloats{dd}, st);
+  if (ddt_bias) launch_sum(p.part_bias, p.B, p.C, p.C, SumFloats{ddt_bias}, st);
+  return launched();
+}
+
+// -------------------------------------------------------------------- norm
+wtconv_status check_norm(const wtconv_norm_desc* d) {
+  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || !dtype_ok(d->io) || !dtype_ok(d->res) || !(d->eps >= 0.f))
+    return WTCONV_ERR_ARG;
+  if ((long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
+  return d->C > WTCONV_NORM_MAX_C || (long long)d->B * d->T > INT_MAX ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
+}
+
+wtconv_status check_norm_inputs(const wtconv_norm_desc* d, const wtconv_rows* x, const wtconv_rows* gate, const float* w,
+                                const wtconv_rows* res, const float* scale, const float* w_res, const int* lengths) {
+  if ((!gate && !w && !res) || (!res && (scale || w_res))) return WTCONV_ERR_ARG;
+  TRY(check_rows(x, elt(d->io), d->B, d->T, d->C, false));
+  if (gate) TRY(check_rows(gate, elt(d->io), d->B, d->T, d->C, false));
+  if (res) TRY(check_rows(res, elt(d->res), d->B, d->T, d->C, false));
+  TRY(check_ptr(w, 4, false));
+  TRY(check_ptr(scale, 4, false));
+  TRY(check_ptr(w_res, 4, false));
+  return check_ptr(lengths, 4, false);
+}
+
+int norm_grad_blocks(const wtconv_norm_desc* d) { return (int)std::min<long long>((long long)d->B * d->T, SMS * 4); }
+
+template <typename IO, typename RES>
+NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, const wtconv_rows* gate, const float* w,
+                            const wtconv_rows* res, const float* scale, const float* w_res, const int* lengths) {
+  NormArgs<IO, RES> a = {};
+  a.x = rows_of<IO>(x);
+  a.gate = rows_of<IO>(gate);
+  a.res = rows_of<RES>(res);
+  a.w = w;
+  a.scale = scale;
+  a.w_res = w_res;
+  a.lengths = lengths;
+  a.B = d->B;
+  a.T = d->T;
+  a.C = d->C;
+  a.eps = d->eps;
+  return a;
+}
+
+// Threads and chunks of a row: few values a thread while a block of 256 holds
+// the row, more for longer rows.  f gets V, NV and the threads.
+template <int V, typename F> wtconv_status norm_shape(int C, F f) {
+  const int chunks = (int)ceil_div(C, V);
+  constexpr int N1 = 8 / V, N2 = 16 / V, N3 = 32 / V;
+  auto threads = [&](int nv) { return (int)ceil_div(ceil_div(chunks, nv), 32) * 32; };
+  if (threads(N1) <= 256) return f(Int<V>(), Int<N1>(), threads(N1));
+  if (threads(N2) <= 512) return f(Int<V>(), Int<N2>(), threads(N2));
+  return f(Int<V>(), Int<N3>(), threads(N3));
+}
+
+template <typename IO, typename RES, typename F> wtconv_status norm_variant(int C, bool vec, F f) {
+  constexpr int V = sizeof(IO) == 2 ? 8 : 4;
+  return vec ? norm_shape<V>(C, f) : norm_shape<1>(C, f);
+}
+
+// Calls f with the I/O type (and the type of the residual).
+template <typename F> wtconv_status with_io(wtconv_dtype io, F f) {
+  return io == WTCONV_F32 ? f(float()) : f(__nv_bfloat16());
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wtconv_causal_workspace_size(const wtconv_causal_desc* desc) {
+  return check_causal(desc) == WTCONV_OK ? causal_ws(desc) : 0;
+}
+
+wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv_rows* x, const float* w,
+                                    const float* bias, const void* state, const int* lengths, const wtconv_rows* y,
+                                    void* state_out, void* stream) {
+  TRY(check_causal(desc));
+  const size_t e = elt(desc->io);
+  const int B = desc->B, T = desc->T, C = desc->C;
+  TRY(check_rows(x, e, B, T, C, false));
+  TRY(check_rows(y, e, B, T, C, true));
+  TRY(check_ptr(w, 4, true));
+  TRY(check_ptr(bias, 4, false));
+  TRY(check_ptr(lengths, 4, false));
+  TRY(check_ptr(state, e, false));
+  TRY(check_ptr(state_out, e, false));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
+    a.y = rows_of<IO>(y);
+    a.state = static_cast<const IO*>(state);
+    a.state_out = static_cast<IO*>(state_out);
+    a.lengths = lengths;
+    a.strips = (int)ceil_div(T, CAUSAL_STRIP);
+    constexpr int V = sizeof(IO) == 2 ? 8 : 4;  // 16 bytes a thread and token
+    const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(y, V, e, B, T) && wide(state, V, e) && wide(state_out, V, e);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return vec ? causal_forward<IO, V>(a, desc->k, st) : causal_forward<IO, 1>(a, desc->k, st);
+  });
+}
+
+wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtconv_rows* x, const wtconv_rows* dy,
+                                     const float* w, const float* bias, const void* state, const int* lengths,
+                                     const void* dstate_out, const wtconv_rows* dx, float* dw, float* dbias,
+                                     void* dstate, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_causal(desc));
+  const size_t e = elt(desc->io);
+  const int B = desc->B, T = desc->T, C = desc->C;
+  TRY(check_rows(x, e, B, T, C, false));
+  TRY(check_rows(dy, e, B, T, C, false));
+  TRY(check_rows(dx, e, B, T, C, true));
+  TRY(check_ptr(w, 4, true));
+  TRY(check_ptr(dw, 4, true));
+  TRY(check_ptr(bias, 4, false));
+  TRY(check_ptr(dbias, 4, bias != nullptr));
+  TRY(check_ptr(lengths, 4, false));
+  TRY(check_ptr(state, e, false));
+  TRY(check_ptr(dstate_out, e, false));
+  TRY(check_ptr(dstate, e, false));
+  TRY(check_ws(ws, ws_bytes, causal_ws(desc)));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
+    a.dy = rows_of<IO>(dy);
+    a.dx = rows_of<IO>(dx);
+    a.state = static_cast<const IO*>(state);
+    a.dstate_out = static_cast<const IO*>(dstate_out);
+    a.dstate = static_cast<IO*>(dstate);
+    a.lengths = lengths;
+    a.part = static_cast<float*>(ws);
+    a.strips = (int)ceil_div(T, CAUSAL_GSTRIP * CAUSAL_GY);
+    constexpr int V = 4;  // taps, windows and sums of 4 channels fill the registers
+    const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(dy, V, e, B, T) && wide(dx, V, e, B, T) &&
+                     wide(state, V, e) && wide(dstate_out, V, e) && wide(dstate, V, e);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return vec ? causal_backward<IO, V>(a, desc->k, dw, dbias, st) : causal_backward<IO, 1>(a, desc->k, dw, dbias, st);
+  });
+}
+
+wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_rows* x, const float* w,
+                                 const float* bias, const int* active, const wtconv_rows* y, void* state,
+                                 void* stream) {
+  TRY(check_causal(desc));
+  if (desc->T != 1) return WTCONV_ERR_ARG;
+  const size_t e = elt(desc->io);
+  const int B = desc->B, C = desc->C;
+  TRY(check_rows(x, e, B, 1, C, false));
+  TRY(check_rows(y, e, B, 1, C, true));
+  TRY(check_ptr(w, 4, true));
+  TRY(check_ptr(bias, 4, false));
+  TRY(check_ptr(active, 4, false));
+  TRY(check_ptr(state, e, desc->k > 1));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
+    a.y = rows_of<IO>(y);
+    a.state_out = static_cast<IO*>(state);
+    constexpr int V = 4;
+    const bool vec = C % V == 0 && wide(x, V, e, B, 1) && wide(y, V, e, B, 1) && wide(state, V, e);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return vec ? causal_step<IO, V>(a, desc->k, active, st) : causal_step<IO, 1>(a, desc->k, active, st);
+  });
+}
+
+size_t wtconv_scan_workspace_size(const wtconv_scan_desc* desc, int backward) {
+  if (check_scan(desc) != WTCONV_OK || (backward != 0 && backward != 1)) return 0;
+  return backward ? rup16(scan_backward_ws(desc).end * sizeof(float)) : 0;
+}
+
+wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_rows* x, const wtconv_rows* dt,
+                                  const float* a, const wtconv_rows* b, const wtconv_rows* c, const float* d,
+                                  const wtconv_rows* z, const float* dt_bias, const float* state, const int* lengths,
+                                  const wtconv_rows* y, float* state_out, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_scan(desc));
+  TRY(check_scan_inputs(desc, x, dt, a, b, c, d, z, dt_bias));
+  TRY(check_rows(y, elt(desc->io), desc->B, desc->T, desc->C, true));
+  TRY(check_ptr(state, 4, false));
+  TRY(check_ptr(state_out, 4, false));
+  TRY(check_ptr(lengths, 4, false));
+  TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 0)));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
+    p.y = rows_of<IO>(y);
+    p.state = state;
+    p.state_out = state_out;
+    p.lengths = lengths;
+    return run_scan_forward<IO, false>(p, static_cast<cudaStream_t>(stream));
+  });
+}
+
+wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_rows* x, const wtconv_rows* dt,
+                                   const float* a, const wtconv_rows* b, const wtconv_rows* c, const float* d,
+                                   const wtconv_rows* z, const float* dt_bias, const float* state, const int* lengths,
+                                   const wtconv_rows* dy, const float* dstate_out, const wtconv_rows* dx,
+                                   const wtconv_rows* ddt, float* da, const wtconv_rows* db, const wtconv_rows* dc,
+                                   float* dd, const wtconv_rows* dz, float* ddt_bias, float* dstate, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  TRY(check_scan(desc));
+  TRY(check_scan_inputs(desc, x, dt, a, b, c, d, z, dt_bias));
+  const size_t e = elt(desc->io);
+  const int B = desc->B, T = desc->T, C = desc->C;
+  const long long gn = (long long)desc->G * desc->N;
+  if ((d != nullptr) != (dd != nullptr) || (z != nullptr) != (dz != nullptr) ||
+      (dt_bias != nullptr) != (ddt_bias != nullptr))
+    return WTCONV_ERR_ARG;
+  TRY(check_rows(dy, e, B, T, C, false));
+  TRY(check_rows(dx, e, B, T, C, true));
+  TRY(check_rows(ddt, e, B, T, C, true));
+  TRY(check_rows(db, e, B, T, gn, true));
+  TRY(check_rows(dc, e, B, T, gn, true));
+  if (dz) TRY(check_rows(dz, e, B, T, C, true));
+  TRY(check_ptr(da, 4, true));
+  TRY(check_ptr(dd, 4, false));
+  TRY(check_ptr(ddt_bias, 4, false));
+  TRY(check_ptr(state, 4, false));
+  TRY(check_ptr(dstate_out, 4, false));
+  TRY(check_ptr(dstate, 4, false));
+  TRY(check_ptr(lengths, 4, false));
+  TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 1)));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
+    p.dy = rows_of<IO>(dy);
+    p.dx = rows_of<IO>(dx);
+    p.ddt = rows_of<IO>(ddt);
+    p.dz = rows_of<IO>(dz);
+    p.state = state;
+    p.dstate_out = dstate_out;
+    p.dstate = dstate;
+    p.lengths = lengths;
+    return run_scan_backward<IO>(desc, p, db, dc, da, dd, ddt_bias, static_cast<float*>(ws),
+                                 static_cast<cudaStream_t>(stream));
+  });
+}
+
+wtconv_status wtconv_scan_step(const wtconv_scan_desc* desc, const wtconv_rows* x, const wtconv_rows* dt,
+                               const float* a, const wtconv_rows* b, const wtconv_rows* c, const float* d,
+                               const wtconv_rows* z, const float* dt_bias, const int* active, const wtconv_rows* y,
+                               float* state, void* stream) {
+  TRY(check_scan(desc));
+  if (desc->T != 1) return WTCONV_ERR_ARG;
+  TRY(check_scan_inputs(desc, x, dt, a, b, c, d, z, dt_bias));
+  TRY(check_rows(y, elt(desc->io), desc->B, 1, desc->C, true));
+  TRY(check_ptr(state, 4, true));
+  TRY(check_ptr(active, 4, false));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
+    p.y = rows_of<IO>(y);
+    p.state_out = state;
+    const long long blocks = ceil_div((long long)p.B * p.C * 4, 128);
+    if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+    scan_step_kernel<IO><<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(p, active);
+    return launched();
+  });
+}
+
+size_t wtconv_norm_workspace_size(const wtconv_norm_desc* desc) {
+  if (check_norm(desc) != WTCONV_OK) return 0;
+  return rup16((size_t)norm_grad_blocks(desc) * 3 * desc->C * sizeof(float));
+}
+
+wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_rows* x, const wtconv_rows* gate,
+                                  const float* w, const wtconv_rows* res, const float* scale, const float* w_res,
+                                  const int* lengths, const wtconv_rows* y, const wtconv_rows* res_out, void* stream) {
+  TRY(check_norm(desc));
+  TRY(check_norm_inputs(desc, x, gate, w, res, scale, w_res, lengths));
+  const int B = desc->B, T = desc->T, C = desc->C;
+  if ((res != nullptr) != (res_out != nullptr) || (!res || w_res ? !y : y != nullptr)) return WTCONV_ERR_ARG;
+  if (y) TRY(check_rows(y, elt(desc->io), B, T, C, true));
+  if (res_out) TRY(check_rows(res_out, elt(desc->res), B, T, C, true));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    return with_io(desc->res, [&](auto rio) {
+      using RES = decltype(rio);
+      NormArgs<IO, RES> a = norm_args<IO, RES>(desc, x, gate, w, res, scale, w_res, lengths);
+      a.y = rows_of<IO>(y);
+      a.res_out = rows_of<RES>(res_out);
+      constexpr int V = sizeof(IO) == 2 ? 8 : 4;
+      const bool vec = C % V == 0 && wide(x, V, sizeof(IO), B, T) && wide(gate, V, sizeof(IO), B, T) &&
+                       wide(y, V, sizeof(IO), B, T) && wide(res, V, sizeof(RES), B, T) &&
+                       wide(res_out, V, sizeof(RES), B, T);
+      return norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
+        norm_forward_kernel<IO, RES, v.value, nv.value>
+            <<<(unsigned)(B * T), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        return launched();
+      });
+    });
+  });
+}
+
+wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_rows* x, const wtconv_rows* gate,
+                                   const float* w, const wtconv_rows* res, const float* scale, const float* w_res,
+                                   const int* lengths, const wtconv_rows* dy, const wtconv_rows* dres_out,
+                                   const wtconv_rows* dx, const wtconv_rows* dgate, float* dw,
+                                   const wtconv_rows* dres, float* dscale, float* dw_res, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  TRY(check_norm(desc));
+  TRY(check_norm_inputs(desc, x, gate, w, res, scale, w_res, lengths));
+  const int B = desc->B, T = desc->T, C = desc->C;
+  if ((gate != nullptr) != (dgate != nullptr) || (w != nullptr) != (dw != nullptr) ||
+      (res != nullptr) != (dres != nullptr) || (scale != nullptr) != (dscale != nullptr) ||
+      (w_res != nullptr) != (dw_res != nullptr) || (dres_out && !res) || (!res || w_res ? !dy : dy != nullptr))
+    return WTCONV_ERR_ARG;
+  if (dy) TRY(check_rows(dy, elt(desc->io), B, T, C, false));
+  if (dres_out) TRY(check_rows(dres_out, elt(desc->res), B, T, C, false));
+  TRY(check_rows(dx, elt(desc->io), B, T, C, true));
+  if (dgate) TRY(check_rows(dgate, elt(desc->io), B, T, C, true));
+  if (dres) TRY(check_rows(dres, elt(desc->res), B, T, C, true));
+  TRY(check_ptr(dw, 4, false));
+  TRY(check_ptr(dscale, 4, false));
+  TRY(check_ptr(dw_res, 4, false));
+  TRY(check_ws(ws, ws_bytes, wtconv_norm_workspace_size(desc)));
+  return with_io(desc->io, [&](auto io) {
+    using IO = decltype(io);
+    return with_io(desc->res, [&](auto rio) {
+      using RES = decltype(rio);
+      NormArgs<IO, RES> a = norm_args<IO, RES>(desc, x, gate, w, res, scale, w_res, lengths);
+      a.dy = rows_of<IO>(dy);
+      a.dres_out = rows_of<RES>(dres_out);
+      a.dx = rows_of<IO>(dx);
+      a.dgate = rows_of<IO>(dgate);
+      a.dres = rows_of<RES>(dres);
+      a.part = static_cast<float*>(ws);
+      constexpr int V = sizeof(IO) == 2 ? 8 : 4;
+      const size_t e = sizeof(IO), re = sizeof(RES);
+      const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(gate, V, e, B, T) && wide(dy, V, e, B, T) &&
+                       wide(dx, V, e, B, T) && wide(dgate, V, e, B, T) && wide(res, V, re, B, T) &&
+                       wide(dres_out, V, re, B, T) && wide(dres, V, re, B, T);
+      cudaStream_t st = static_cast<cudaStream_t>(stream);
+      const int blocks = norm_grad_blocks(desc);
+      TRY((norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
+        norm_backward_kernel<IO, RES, v.value, nv.value><<<blocks, threads, 0, st>>>(a);
+        return launched();
+      })));
+      if (!dw && !dscale && !dw_res) return WTCONV_OK;
+      launch_sum(a.part, blocks, 3ll * C, 3ll * C, NormSums{dw, dscale, dw_res, C}, st);
+      return launched();
+    });
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,133 @@
+// Shared pieces of the sequence kernels: I/O types, rows of an activation,
+// the gate functions and the fixed-order sum of per-block partials.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "wtconv_seq.h"
+
+namespace wtseq {
+
+template <typename IO> __device__ __forceinline__ float to_f(IO v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+// One rounding to nearest even, of outputs only: relative error 2^-9.
+template <typename IO> __device__ __forceinline__ IO from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Rows of an activation, strides in elements (64-bit: a cache may hold more
+// than 2^31 elements).
+template <typename IO> struct Rows {
+  IO* p;
+  long long sb, st;
+  __device__ __forceinline__ IO* at(int b, long long t) const { return p + b * sb + t * st; }
+};
+
+template <typename IO> inline Rows<IO> rows_of(const wtconv_rows* r) {
+  if (!r) return Rows<IO>{nullptr, 0, 0};
+  return Rows<IO>{static_cast<IO*>(r->data), r->batch_stride, r->token_stride};
+}
+
+// V consecutive channels in accesses of up to 16 bytes, which they are aligned
+// to, and as fp32 values.
+template <typename IO, int V> struct alignas(sizeof(IO) * V <= 16 ? sizeof(IO) * V : 16) Pack { IO v[V]; };
+
+template <typename IO, int V> __device__ __forceinline__ void load_pack(const IO* p, float (&f)[V]) {
+  constexpr int W = sizeof(IO) * V <= 16 ? V : 16 / sizeof(IO);
+#pragma unroll
+  for (int k = 0; k < V; k += W) {
+    const Pack<IO, W> r = *reinterpret_cast<const Pack<IO, W>*>(p + k);
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[k + i] = to_f<IO>(r.v[i]);
+  }
+}
+template <typename IO, int V> __device__ __forceinline__ void store_pack(IO* p, const float (&f)[V]) {
+  constexpr int W = sizeof(IO) * V <= 16 ? V : 16 / sizeof(IO);
+#pragma unroll
+  for (int k = 0; k < V; k += W) {
+    Pack<IO, W> r;
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.v[i] = from_f<IO>(f[k + i]);
+    *reinterpret_cast<Pack<IO, W>*>(p + k) = r;
+  }
+}
+
+__device__ __forceinline__ int row_length(const int* lengths, int b, int T) {
+  if (!lengths) return T;
+  const int n = __ldg(lengths + b);
+  return n < 0 ? 0 : (n < T ? n : T);
+}
+
+// 1 / (1 + exp(-v)): exp overflows to infinity for v < -88, and the quotient
+// is then the zero that it should be.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+// d silu(v) / dv, given sigmoid(v)
+__device__ __forceinline__ float dsilu(float v, float sg) { return sg * (1.f + v * (1.f - sg)); }
+
+// log(1 + e) for 0 <= e <= 1 as 2 atanh(s), s = e / (2 + e) <= 1/3, by the
+// Taylor series of atanh: the first term left out is below 2^-25 of the sum.
+// (log(1 + e) from the rounded sum 1 + e would lose the small e, and with
+// them the step sizes near 1e-3 that a scan lives on.)
+__device__ __forceinline__ float log1p_unit(float e) {
+  const float s = __fdividef(e, 2.f + e), q = s * s;
+  float r = 2.f / 15.f;
+  r = fmaf(r, q, 2.f / 13.f);
+  r = fmaf(r, q, 2.f / 11.f);
+  r = fmaf(r, q, 2.f / 9.f);
+  r = fmaf(r, q, 2.f / 7.f);
+  r = fmaf(r, q, 2.f / 5.f);
+  r = fmaf(r, q, 2.f / 3.f);
+  r = fmaf(r, q, 2.f);
+  return s * r;
+}
+
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); NaN stays NaN (v > 0 is then
+// false, and the sum takes it from exp).
+__device__ __forceinline__ float softplus(float v) {
+  return (v > 0.f ? v : 0.f) + log1p_unit(__expf(-fabsf(v)));
+}
+
+// out[i] = sum over p of part[p * stride + i] in a fixed order: a block holds
+// 32 outputs x 8 slices of p, each summed in order, the slices joined in order.
+struct SumFloats {
+  float* out;
+  __device__ __forceinline__ void put(long long i, float v) const { out[i] = v; }
+};
+template <typename IO> struct SumRows {  // i = (b * T + t) * W + w
+  Rows<IO> out;
+  int T, W;
+  __device__ __forceinline__ void put(long long i, float v) const {
+    const long long r = i / W;
+    out.at((int)(r / T), r % T)[i % W] = from_f<IO>(v);
+  }
+};
+
+template <typename Target>
+__global__ void __launch_bounds__(256) sum_partials(const float* __restrict__ part, long long P, long long stride, long long n, Target target) {
+  __shared__ float s[8][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const long long i = (long long)blockIdx.x * 32 + x;
+  float v = 0.f;
+  if (i < n) {
+    const long long per = (P + 7) / 8, p1 = (y + 1) * per < P ? (y + 1) * per : P;
+    for (long long p = y * per; p < p1; ++p) v += __ldg(part + p * stride + i);
+  }
+  s[y][x] = v;
+  __syncthreads();
+  if (y == 0 && i < n) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += s[k][x];
+    target.put(i, v);
+  }
+}
+
+template <typename Target>
+inline void launch_sum(const float* part, long long P, long long stride, long long n, Target t, cudaStream_t st) {
+  sum_partials<Target><<<(unsigned)((n + 31) / 32), 256, 0, st>>>(part, P, stride, n, t);
+}
+
+}  // namespace wtseq

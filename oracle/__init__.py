@@ -7,3 +7,4 @@ from .wtconv_oracle import (  # noqa: F401
     BANDS, SIGN, haar_analysis, haar_synthesis, dwconv, dwcorr_weight,
     forward, backward, analysis_closed_form, synthesis_closed_form, level_outputs,
 )
+from . import seq_oracle  # noqa: F401

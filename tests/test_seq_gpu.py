@@ -1,0 +1,410 @@
+"""The sequence operators on the GPU against the float64 oracle.
+
+Every value is held to the rounding of its type plus, for the operations in
+the longest chain behind it, one 32-bit error each relative to the sum of its
+terms' absolute values (tests/seq_cases.py)."""
+import pytest
+import torch
+
+import depthwise_convolution_wtconv_b200 as wt
+import seq_cases as sc
+from seq_cases import causal_case, causal_oracle, check, cuda, norm_case, norm_oracle, scan_case, scan_ops, scan_oracle
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ causal
+# strips are 32 tokens, gradient blocks 256; vectors 8, 4 or 1 channels
+CAUSAL = [
+    dict(B=1, T=1, C=8, k=4, io="f32"),
+    dict(B=2, T=2, C=16, k=4, io="bf16"),                      # shorter than the taps
+    dict(B=3, T=33, C=7, k=3, io="bf16", ragged=True),         # odd channels, one token in the last strip
+    dict(B=4, T=31, C=20, k=2, io="f32", ragged=True, state=False),
+    dict(B=2, T=64, C=136, k=5, io="bf16", state=False),
+    dict(B=2, T=65, C=260, k=8, io="f32", ragged=True),
+    dict(B=1, T=300, C=36, k=7, io="bf16", bias=False),        # a second gradient block, no bias
+    dict(B=5, T=257, C=3, k=6, io="f32", ragged=True),
+    dict(B=2, T=40, C=24, k=1, io="f32", ragged=True),         # no state at all
+]
+
+
+def _name(c):
+    return "-".join(f"{k}{v}" for k, v in c.items())
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("case", CAUSAL, ids=_name)
+def test_causal_forward(cuda_ok, case, silu):
+    s = causal_case(**case)
+    d = cuda(s)
+    y, state = wt.causal_forward(d["x"], d["w"], d["b"], silu=silu, state=d["state"], lengths=d["lengths"])
+    want, size = causal_oracle(s, silu), causal_oracle(s, silu, mag=True)
+    check(y, want["y"], size["y"], case["k"] + 8, "y")
+    assert torch.equal(state.double().cpu(), torch.from_numpy(want["state"]))
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("case", CAUSAL, ids=_name)
+def test_causal_backward(cuda_ok, case, silu):
+    s = causal_case(**case)
+    d = cuda(s)
+    dx, g = wt.causal_backward(d["x"], d["dy"], d["w"], d["b"], silu=silu, state=d["state"], lengths=d["lengths"],
+                               dstate=d["dstate"])
+    want, size = causal_oracle(s, silu, True), causal_oracle(s, silu, True, mag=True)
+    k, n = case["k"], case["B"] * case["T"]
+    check(dx, want["dx"], size["dx"], 2 * k + 10, "dx")
+    check(g["dw"], want["dw"], size["dw"], k + 10 + n / 8, "dw")
+    check(g["db"], None if s["b"] is None else want["db"], size["db"], k + 10 + n / 8, "db")
+    check(g["dstate"], None if s["state"] is None else want["dstate"], size["dstate"], 2 * k + 10, "dstate")
+
+
+@pytest.mark.parametrize("io,B,C,k", [("f32", 1, 8, 4), ("bf16", 5, 36, 4), ("bf16", 3, 7, 3), ("f32", 2, 130, 8), ("f32", 2, 4, 1)])
+def test_causal_step_equals_the_prompt(cuda_ok, io, B, C, k):
+    """Token by token gives the outputs and states of the whole prompt, bit for bit; rows that are not active keep theirs."""
+    T = 9
+    d = cuda(causal_case(B, T, C, k, io, seed=2))
+    y, state = wt.causal_forward(d["x"], d["w"], d["b"], state=d["state"])
+    s = d["state"].clone()
+    for t in range(T):
+        assert torch.equal(wt.causal_step(d["x"][:, t], s, d["w"], d["b"]), y[:, t])
+    assert torch.equal(s, state)
+    before = s.clone()
+    active = (torch.arange(B, device="cuda") % 2).to(torch.int32)
+    out = wt.causal_step(d["x"][:, 0], s, d["w"], d["b"], active=active)
+    on = active.bool()
+    assert not out[~on].any() and torch.equal(s[~on], before[~on])
+    if k > 1:
+        assert torch.equal(s[on][:, -1], d["x"][:, 0][on])
+
+
+def test_causal_prompt_in_pieces(cuda_ok):
+    """A prompt cut into pieces, the state handed on in place, gives the same outputs."""
+    d = cuda(causal_case(2, 100, 24, 4, "bf16", seed=5))
+    y, state = wt.causal_forward(d["x"], d["w"], d["b"], state=d["state"])
+    s, t = d["state"].clone(), 0
+    for n in (1, 2, 34, 0, 63):
+        if n:
+            piece, _ = wt.causal_forward(d["x"][:, t:t + n], d["w"], d["b"], state=s, state_out=s)
+            assert torch.equal(piece, y[:, t:t + n])
+        t += n
+    assert torch.equal(s, state)
+
+
+# -------------------------------------------------------------------- scan
+# tiles are 16 tokens, blocks 32 channels
+SCAN = [
+    dict(B=1, T=1, C=8, N=4, io="f32"),
+    dict(B=2, T=3, C=33, N=16, io="bf16"),                              # one channel in the second block
+    dict(B=3, T=17, C=64, N=16, io="f32", ragged=True),
+    dict(B=4, T=48, C=30, N=13, io="bf16", ragged=True, G=2),            # two groups of 15 channels, odd states
+    dict(B=2, T=37, C=96, N=1, io="f32", G=3, state=False),
+    dict(B=1, T=130, C=40, N=64, io="f32", z=False),
+    dict(B=2, T=64, C=32, N=16, io="bf16", d=False, bias=False, state=False),
+    dict(B=3, T=300, C=20, N=5, io="f32", ragged=True),
+    dict(B=1, T=600, C=34, N=8, io="f32", slow=True),                   # states that hardly decay
+    dict(B=5, T=50, C=2, N=3, io="bf16", ragged=True, G=2, z=False, d=False),
+    dict(B=1, T=1100, C=16, N=16, io="bf16"),
+]
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("case", SCAN, ids=_name)
+def test_scan_forward(cuda_ok, case, softplus):
+    s = _scan_inputs(case, softplus)
+    d = cuda(s)
+    y, state = wt.scan_forward(d["x"], d["dt"], d["a"], d["b"], d["c"], d["d"], d["z"], d["dt_bias"], softplus=softplus,
+                               state=d["state"], lengths=d["lengths"])
+    want, size = scan_oracle(s, softplus), scan_oracle(s, softplus, mag=True)
+    ops = scan_ops(case["B"], case["T"], case["C"], case["N"])
+    check(y, want["y"], size["y"], ops, "y")
+    check(state, want["state"], size["state"], ops, "state")
+
+
+def _scan_inputs(case, softplus):
+    s = scan_case(**case)
+    if not softplus:  # step sizes as they are: positive, and small without the bias too
+        s["dt"] = (0.05 * s["dt"].abs()).to(s["dt"].dtype)
+        s["dt_bias"] = None if s["dt_bias"] is None else 0.01 * s["dt_bias"].abs()
+    return s
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("case", SCAN, ids=_name)
+def test_scan_backward(cuda_ok, case, softplus):
+    s = _scan_inputs(case, softplus)
+    d = cuda(s)
+    g = wt.scan_backward(d["x"], d["dt"], d["a"], d["b"], d["c"], d["dy"], d["d"], d["z"], d["dt_bias"], softplus=softplus,
+                         state=d["state"], lengths=d["lengths"], dstate=d["dstate"])
+    want, size = scan_oracle(s, softplus, True), scan_oracle(s, softplus, True, mag=True)
+    ops = 2 * scan_ops(case["B"], case["T"], case["C"], case["N"])  # there and back
+    given = dict(dd=s["d"], dz=s["z"], ddt_bias=s["dt_bias"], dstate=s["state"])
+    for m in ("dx", "ddt", "da", "db", "dc", "dd", "dz", "ddt_bias", "dstate"):
+        check(g[m], None if m in given and given[m] is None else want.get(m), size.get(m), ops, m)
+
+
+@pytest.mark.parametrize("io,B,C,N,G", [("f32", 1, 8, 16, 1), ("bf16", 5, 36, 16, 2), ("bf16", 3, 7, 5, 1), ("f32", 2, 130, 64, 1),
+                                        ("f32", 3, 6, 1, 3)])
+def test_scan_step(cuda_ok, io, B, C, N, G):
+    """Steps against the oracle's pass over the same tokens; rows that are not active keep their state."""
+    T = 5
+    s = scan_case(B, T, C, N, io, G=G, seed=4)
+    d = cuda(s)
+    state = d["state"].clone()
+    ys = [wt.scan_step(d["x"][:, t], d["dt"][:, t], state, d["a"], d["b"][:, t], d["c"][:, t], d["d"], d["z"][:, t], d["dt_bias"])
+          for t in range(T)]
+    want, size = scan_oracle(s), scan_oracle(s, mag=True)
+    ops = scan_ops(B, T, C, N)
+    check(torch.stack(ys, 1), want["y"], size["y"], ops, "y")
+    check(state, want["state"], size["state"], ops, "state")
+    before = state.clone()
+    active = (torch.arange(B, device="cuda") % 2).to(torch.int32)
+    out = wt.scan_step(d["x"][:, 0], d["dt"][:, 0], state, d["a"], d["b"][:, 0], d["c"][:, 0], d["d"], d["z"][:, 0], d["dt_bias"],
+                       active=active)
+    off = ~active.bool()
+    assert not out[off].any() and torch.equal(state[off], before[off])
+    assert B == 1 or not torch.equal(state[~off], before[~off])
+
+
+def test_scan_prompt_in_pieces(cuda_ok):
+    """A prompt in pieces, the state handed on in place: the pieces' last state is the prompt's, and so are the outputs."""
+    s = scan_case(2, 150, 40, 16, "f32", seed=6)
+    d = cuda(s)
+    st, t, ys = d["state"].clone(), 0, []
+    for n in (1, 16, 50, 83):
+        cut = {m: d[m][:, t:t + n] for m in ("x", "dt", "b", "c", "z")}
+        y, _ = wt.scan_forward(cut["x"], cut["dt"], d["a"], cut["b"], cut["c"], d["d"], cut["z"], d["dt_bias"], state=st, state_out=st)
+        ys.append(y)
+        t += n
+    want, size = scan_oracle(s), scan_oracle(s, mag=True)
+    check(torch.cat(ys, 1), want["y"], size["y"], scan_ops(2, 150, 40, 16), "y")
+    check(st, want["state"], size["state"], scan_ops(2, 150, 40, 16), "state")
+
+
+# -------------------------------------------------------------------- norm
+NORM = [
+    dict(B=1, T=1, C=1, io="f32"),
+    dict(B=2, T=3, C=7, io="bf16", res="bf16"),
+    dict(B=3, T=5, C=64, io="bf16", res="f32", ragged=True),
+    dict(B=1, T=4, C=2048, io="bf16", res="f32"),
+    dict(B=2, T=2, C=2056, io="bf16", res="bf16"),              # past one chunk a thread
+    dict(B=1, T=3, C=8200, io="f32", res="f32"),
+    dict(B=1, T=2, C=16384, io="bf16", res="f32"),              # the longest row
+    dict(B=1, T=2, C=16383, io="bf16", res="bf16"),             # the longest odd row
+    dict(B=2, T=350, C=40, io="f32", res="bf16", ragged=True),   # more rows than blocks in the gradient
+    dict(B=2, T=3, C=100, io="f32", gate=False),
+    dict(B=2, T=3, C=100, io="bf16", w=False),
+    dict(B=2, T=3, C=100, io="bf16", res="f32", gate=False, w=False),
+    dict(B=2, T=3, C=100, io="f32", res="f32", scale=False, gate=False),
+    dict(B=2, T=3, C=100, io="f32", res="f32", w_res=False, ragged=True),
+]
+
+
+@pytest.mark.parametrize("case", NORM, ids=_name)
+def test_norm_forward(cuda_ok, case):
+    s = norm_case(**case)
+    d = cuda(s)
+    y, res = wt.norm_forward(d["x"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], lengths=d["lengths"])
+    want, size = norm_oracle(s), norm_oracle(s, mag=True)
+    ops = 24 + case["C"] / 8
+    check(y, want["y"], size["y"], ops, "y")
+    check(res, want["res"], size["res"], ops, "res")
+
+
+@pytest.mark.parametrize("case", NORM, ids=_name)
+def test_norm_backward(cuda_ok, case):
+    s = norm_case(**case)
+    d = cuda(s)
+    g = wt.norm_backward(d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], dres=d["dres"], lengths=d["lengths"])
+    want, size = norm_oracle(s, True), norm_oracle(s, True, mag=True)
+    ops = 2 * (24 + case["C"] / 8) + case["B"] * case["T"] / 8
+    given = dict(dgate=s["gate"], dw=s["w"], dres=s["res"], dscale=s["scale"], dw_res=s["w_res"])
+    for m in ("dx", "dgate", "dw", "dres", "dscale", "dw_res"):
+        check(g[m], None if m in given and given[m] is None else want.get(m), size.get(m), ops, m)
+
+
+def test_norm_of_single_tokens(cuda_ok):
+    """[B, C] inputs are rows of one token."""
+    s = norm_case(7, 1, 96, "bf16", res="f32", seed=3)
+    d = cuda(s)
+    flat = {m: d[m][:, 0] for m in ("x", "gate", "res", "dy", "dres")}
+    y, res = wt.norm_forward(d["x"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"])
+    y2, res2 = wt.norm_forward(flat["x"], d["w"], flat["gate"], flat["res"], d["scale"], d["w_res"])
+    assert torch.equal(y[:, 0], y2) and torch.equal(res[:, 0], res2)
+
+
+def test_norm_without_dres(cuda_ok):
+    """No gradient for res_out is a zero gradient."""
+    d = cuda(norm_case(2, 3, 24, "f32", res="f32"))
+    args = (d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"])
+    a, b = wt.norm_backward(*args), wt.norm_backward(*args, dres=torch.zeros_like(d["dres"]))
+    for m in a:
+        assert torch.equal(a[m], b[m]), m
+
+
+# ------------------------------------------------- shared by the operators
+def _calls(io, C=24, T=50, B=3, view=lambda t: t):
+    """Every call with fixed inputs, as functions that give all their outputs; `view` lays out the activations."""
+    a, s, n = causal_case(B, T, C, 4, io), scan_case(B, T, C, 8, io, G=2), norm_case(B, T, C, io, res="f32")
+    c, s, n = cuda(a), cuda(s), cuda(n)
+    lens = torch.tensor([T, 0, T // 2], dtype=torch.int32, device="cuda")
+    for d in (c, s, n):
+        for m in ("x", "dt", "z", "b", "c", "dy", "gate", "res", "dres"):
+            if isinstance(d.get(m), torch.Tensor) and d[m].dim() >= 3:
+                d[m] = view(d[m])
+    flat = lambda r: [t for p in r for t in (p.values() if isinstance(p, dict) else [p]) if t is not None]
+    step = lambda d, ms: {m: d[m][:, 0] for m in ms}
+    st, sx = step(c, "x"), step(s, ("x", "dt", "b", "c", "z"))
+
+    def causal_step(**k):
+        held = c["state"].clone()
+        return [wt.causal_step(st["x"], held, c["w"], c["b"], **k), held]
+
+    def scan_step(**k):
+        held = s["state"].clone()
+        return [wt.scan_step(sx["x"], sx["dt"], held, s["a"], sx["b"], sx["c"], s["d"], sx["z"], s["dt_bias"], **k), held]
+    ins = (s["x"], s["dt"], s["a"], s["b"], s["c"])
+    return dict(
+        causal_forward=lambda **k: flat(wt.causal_forward(c["x"], c["w"], c["b"], state=c["state"], lengths=lens, **k)),
+        causal_backward=lambda **k: flat(wt.causal_backward(c["x"], c["dy"], c["w"], c["b"], state=c["state"], lengths=lens,
+                                                            dstate=c["dstate"], **k)),
+        causal_step=causal_step, scan_step=scan_step,
+        scan_forward=lambda **k: flat(wt.scan_forward(*ins, s["d"], s["z"], s["dt_bias"], state=s["state"], lengths=lens, **k)),
+        scan_backward=lambda **k: flat([wt.scan_backward(*ins, s["dy"], s["d"], s["z"], s["dt_bias"], state=s["state"], lengths=lens,
+                                                         dstate=s["dstate"], **k)]),
+        norm_forward=lambda **k: flat(wt.norm_forward(n["x"], n["w"], n["gate"], n["res"], n["scale"], n["w_res"], lengths=lens, **k)),
+        norm_backward=lambda **k: flat([wt.norm_backward(n["x"], n["dy"], n["w"], n["gate"], n["res"], n["scale"], n["w_res"],
+                                                         dres=n["dres"], lengths=lens, **k)]),
+    )
+
+
+OPS = ("causal_forward", "causal_backward", "causal_step", "scan_forward", "scan_backward", "scan_step", "norm_forward",
+       "norm_backward")
+
+
+def _half(t):
+    """The values of t as the first part of wider rows."""
+    wide = torch.zeros(*t.shape[:2], t[0, 0].numel() * 2 + 8, dtype=t.dtype, device=t.device)
+    part = wide[..., : t[0, 0].numel()]
+    part.copy_(t.flatten(2))
+    return part.unflatten(-1, t.shape[2:])
+
+
+def _odd(t):
+    """... as rows that begin at odd addresses."""
+    wide = torch.zeros(*t.shape[:2], t[0, 0].numel() + 3, dtype=t.dtype, device=t.device)
+    part = wide[..., 1: 1 + t[0, 0].numel()]
+    part.copy_(t.flatten(2))
+    return part.unflatten(-1, t.shape[2:])
+
+
+def _token_major(t):
+    """... with the batch inside the tokens."""
+    return t.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("view", [_half, _odd, _token_major], ids=["half", "odd", "token_major"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("op", OPS)
+def test_strided_inputs_give_the_same(cuda_ok, op, io, view):
+    """The layout of the inputs changes no result beyond the order of a sum."""
+    want, got = _calls(io)[op](), _calls(io, view=view)[op]()
+    for a, b in zip(want, got):
+        tol = 2 * sc.HALF[a.dtype] + 2.0 ** -18
+        assert torch.allclose(a.double(), b.double(), rtol=tol, atol=tol * float(a.double().abs().max() + 1e-30))
+
+
+def test_strided_outputs(cuda_ok):
+    """Outputs go into halves of wider rows and leave the rest of them alone."""
+    d = cuda(causal_case(2, 40, 16, 4, "bf16"))
+    want, _ = wt.causal_forward(d["x"], d["w"], d["b"])
+    wide = torch.full((2, 40, 48), 7.0, dtype=torch.bfloat16, device="cuda")
+    wt.causal_forward(d["x"], d["w"], d["b"], y=wide[..., 16:32])
+    assert torch.equal(wide[..., 16:32], want) and (wide[..., :16] == 7).all() and (wide[..., 32:] == 7).all()
+    s = cuda(scan_case(2, 40, 16, 8, "f32"))
+    args = (s["x"], s["dt"], s["a"], s["b"], s["c"], s["dy"], s["d"], s["z"], s["dt_bias"])
+    g = wt.scan_backward(*args)
+    wide = torch.full((2, 40, 80), 7.0, device="cuda")  # ddt, db and dc as one projection's output gradient
+    h = dict(dx=torch.empty_like(g["dx"]), ddt=wide[..., :16], da=torch.empty_like(g["da"]), db=wide[..., 16:24].unflatten(-1, (1, 8)),
+             dc=wide[..., 24:32].unflatten(-1, (1, 8)), dd=torch.empty_like(g["dd"]), dz=wide[..., 64:], ddt_bias=torch.empty_like(g["dd"]),
+             dstate=None)
+    wt.scan_backward(*args, grads=h)
+    for m in ("dx", "ddt", "da", "db", "dc", "dd", "dz", "ddt_bias"):
+        assert torch.equal(g[m], h[m]), m
+    assert (wide[..., 32:64] == 7).all()
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_repeats_streams_and_graphs(cuda_ok, op):
+    """The same bits again, on another stream, and from a captured graph that is replayed."""
+    call = _calls("bf16", C=72, T=130)[op]
+    want = call()
+    for a, b in zip(want, call()):
+        assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(stream=side)
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    for t in held:
+        t.fill_(9)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, held):
+        assert torch.equal(a, b)
+
+
+def test_two_captured_graphs_with_one_workspace(cuda_ok):
+    """A workspace carries nothing from call to call: two graphs may share one, replayed in turn on one stream."""
+    cases = [cuda(scan_case(2, 70, 48, 8, "f32", seed=i)) for i in range(2)]
+    call = lambda s, ws: wt.scan_backward(s["x"], s["dt"], s["a"], s["b"], s["c"], s["dy"], s["d"], s["z"], s["dt_bias"], ws=ws)
+    want = [call(s, None) for s in cases]
+    from depthwise_convolution_wtconv_b200 import _seq
+    ws = torch.empty(wt.load_seq().wtconv_scan_workspace_size(_seq.ScanDesc(2, 70, 48, 8, 1, 0, 1), 1), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for s in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(s, ws))
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        for m in w:
+            assert w[m] is None and o[m] is None or torch.equal(w[m], o[m]), m
+
+
+def test_binding_refusals(cuda_ok):
+    x, w = torch.zeros(2, 4, 8, device="cuda"), torch.zeros(8, 4, device="cuda")
+    with pytest.raises(TypeError):
+        wt.causal_forward(x.half(), w)
+    with pytest.raises(ValueError, match="shape"):
+        wt.causal_forward(x, w[:4])
+    with pytest.raises(ValueError, match="contiguous"):
+        wt.causal_forward(x.transpose(1, 2).contiguous().transpose(1, 2), w)
+    with pytest.raises(TypeError, match="lengths"):
+        wt.causal_forward(x, w, lengths=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="state"):
+        wt.causal_forward(x, w, state=torch.zeros(2, 4, 8, device="cuda"))
+    with pytest.raises(wt.WTConvError, match="ARG"):
+        wt.causal_forward(x, w, y=x[:, :1].expand(2, 4, 8).detach())
+    with pytest.raises(wt.WTConvError, match="UNSUPPORTED"):
+        wt.causal_forward(x, torch.zeros(8, 9, device="cuda"))
+    b = torch.zeros(2, 4, 16, device="cuda")
+    a = torch.zeros(8, 16, device="cuda")
+    with pytest.raises(ValueError, match="c must have shape"):
+        wt.scan_forward(x, x, a, b, b[..., :8])
+    with pytest.raises(wt.WTConvError, match="ARG"):
+        wt.scan_forward(x, x, a, b.view(2, 4, 1, 16).expand(2, 4, 3, 16).contiguous(), b.view(2, 4, 1, 16).expand(2, 4, 3, 16).contiguous())
+    with pytest.raises(wt.WTConvError, match="WORKSPACE"):
+        wt.scan_backward(x, x, a, b, b, x, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(wt.WTConvError, match="ARG"):
+        wt.norm_forward(x)
+    with pytest.raises(wt.WTConvError, match="ARG"):
+        wt.norm_backward(x, None, torch.ones(8, device="cuda"))
