@@ -187,6 +187,10 @@ ScanArgs<IO> scan_args(const wtconv_scan_desc* d, const wtconv_rows* x, const wt
   p.softplus = d->softplus;
   p.blocks = scan_blocks(d);
   p.tiles = (int)ceil_div(d->T, SCAN_T);
+  const size_t e = sizeof(IO);
+  const int V = 16 / sizeof(IO);
+  p.wide_x = (d->C / d->G) % V == 0 && wide(x, V, e, d->B, d->T) && wide(dt, V, e, d->B, d->T) && wide(z, V, e, d->B, d->T);
+  p.wide_bc = d->N % V == 0 && wide(b, V, e, d->B, d->T) && wide(c, V, e, d->B, d->T);
   return p;
 }
 
@@ -212,14 +216,44 @@ template <typename K> wtconv_status allow_smem(K kernel, size_t bytes) {
              : WTCONV_ERR_CUDA;
 }
 
-template <typename IO, bool CKPT> wtconv_status run_scan_forward(const ScanArgs<IO>& p, cudaStream_t st) {
-  const long long blocks = (long long)p.B * p.blocks * p.G;
+// Chunks of a row: as many as it takes to give every SM SCAN_FILL blocks, of
+// at least SCAN_CHUNK tiles.  A cut row pays the recurrence twice, so rows are
+// cut only where whole ones leave half of that idle.
+constexpr int SCAN_FILL = 4, SCAN_CHUNK = 4;
+void scan_plan(const wtconv_scan_desc* d, int* chunks, int* chunk_tiles) {
+  const long long rows = (long long)d->B * scan_blocks(d) * d->G, tiles = ceil_div(d->T, SCAN_T);
+  long long n = 1;
+  if (rows * 2 <= SMS * SCAN_FILL) n = std::max(1ll, std::min(SMS * SCAN_FILL / rows, tiles / SCAN_CHUNK));
+  *chunk_tiles = (int)ceil_div(tiles, n);
+  *chunks = (int)ceil_div(tiles, *chunk_tiles);
+}
+// Floats of the chunks' ends and sums (0: rows are not cut).
+size_t scan_chunk_floats(const wtconv_scan_desc* d) {
+  int chunks, per;
+  scan_plan(d, &chunks, &per);
+  return chunks == 1 ? 0 : (size_t)chunks * d->B * d->C * (d->N + 1);
+}
+
+template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>& p, cudaStream_t st) {
+  const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
-  const size_t smem =
-      sizeof(float) * (2 * SCAN_T * 32 + (CKPT ? 0 : SCAN_W * SCAN_T * 32) + 2 * p.N * SCAN_LD + 2 * p.N * 32);
-  TRY(allow_smem(scan_forward_kernel<IO, CKPT>, smem));
-  scan_forward_kernel<IO, CKPT><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
+  const ScanSmem<IO> s(nullptr, p.N);
+  const size_t smem = s.end - (char*)nullptr;
+  TRY(allow_smem(scan_forward_kernel<IO, MODE>, smem));
+  scan_forward_kernel<IO, MODE><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
   return launched();
+}
+
+// The chunks' ends where rows are cut, then y or the states before each tile.
+template <typename IO, int MODE>
+wtconv_status run_scan_forward(const wtconv_scan_desc* d, ScanArgs<IO>& p, float* chunk_ws, cudaStream_t st) {
+  scan_plan(d, &p.chunks, &p.chunk_tiles);
+  if (p.chunks > 1) {
+    p.ends = chunk_ws;
+    p.sums = chunk_ws + (size_t)p.chunks * p.B * p.C * p.N;
+    TRY((run_scan_pass<IO, SCAN_ENDS>(p, st)));
+  }
+  return run_scan_pass<IO, MODE>(p, st);
 }
 
 // Sums of db or dc: output i = ((g * B + b) * T + t) * N + n
@@ -245,7 +279,8 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
   p.part_a = ws + w.part_a;
   p.part_d = ws + w.part_d;
   p.part_bias = ws + w.part_bias;
-  TRY((run_scan_forward<IO, true>(p, st)));
+  TRY((run_scan_forward<IO, SCAN_CKPT>(d, p, ws + w.end, st)));
+  p.chunks = 1;
   const long long blocks = (long long)p.B * p.blocks * p.G;
   const size_t smem = sizeof(float) * (3 * SCAN_T * 32 + 3 * SCAN_W * SCAN_T * 32 + 2 * p.N * SCAN_LD + 3 * p.N * 32);
   TRY(allow_smem(scan_backward_kernel<IO>, smem));
@@ -423,7 +458,7 @@ wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_ro
 
 size_t wtconv_scan_workspace_size(const wtconv_scan_desc* desc, int backward) {
   if (check_scan(desc) != WTCONV_OK || (backward != 0 && backward != 1)) return 0;
-  return backward ? rup16(scan_backward_ws(desc).end * sizeof(float)) : 0;
+  return rup16(((backward ? scan_backward_ws(desc).end : 0) + scan_chunk_floats(desc)) * sizeof(float));
 }
 
 wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_rows* x, const wtconv_rows* dt,
@@ -444,7 +479,7 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
     p.state = state;
     p.state_out = state_out;
     p.lengths = lengths;
-    return run_scan_forward<IO, false>(p, static_cast<cudaStream_t>(stream));
+    return run_scan_forward<IO, SCAN_Y>(desc, p, static_cast<float*>(ws), static_cast<cudaStream_t>(stream));
   });
 }
 

@@ -10,6 +10,11 @@
 //   C  the warps share out the tokens again, join the warps' sums and apply
 //      d x and the gate.
 // Tokens behind a row's length get delta = 0, x = 0: they leave h as it is.
+//
+// Rows of which there are too few to fill the GPU are cut into chunks of
+// tiles, each chunk a block: a first pass finds each chunk's state from a zero
+// start and its sum of delta (the decay over the chunk is exp(a sum delta)),
+// and every chunk of the second pass joins those before it into its start.
 #pragma once
 
 #include "seq_common.cuh"
@@ -18,9 +23,11 @@ namespace wtseq {
 
 constexpr int SCAN_T = 16;        // tokens of a tile
 constexpr int SCAN_W = 4;         // warps of a block
-constexpr int SCAN_R = SCAN_T / SCAN_W;  // tokens of a warp in A and C
+constexpr int SCAN_R = SCAN_T / SCAN_W;  // tokens of a warp in A and C: one float4
 constexpr int SCAN_LD = SCAN_T + 4;      // floats between states in the b, c tiles
+constexpr int SCAN_SLOTS = 4;            // tiles of inputs in shared memory
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+static_assert(SCAN_R == 4, "a thread's tokens of a tile are one float4");
 
 template <typename IO> struct ScanArgs {
   Rows<IO> x, dt, z, b, c, y, dy, dx, ddt, dz;
@@ -29,23 +36,323 @@ template <typename IO> struct ScanArgs {
   const float* dstate_out;
   float* dstate;
   const int* lengths;
+  float* ends;               // [chunks][B][N][C] states after each chunk from a zero start
+  float* sums;               // [chunks][B][C] sums of delta over each chunk
   float* ckpt;               // [B][tiles][N][C] states before each tile
   float *part_b, *part_c;    // [C blocks][B][T][N]
   float *part_a;             // [B][C][N]
   float *part_d, *part_bias; // [B][C]
   int B, T, C, N, G, softplus;
-  int blocks;  // blocks of 32 channels in a group
-  int tiles;
+  int blocks;       // blocks of 32 channels in a group
+  int tiles;        // of a row
+  int chunks;       // of a row
+  int chunk_tiles;  // of a chunk
+  int wide_x;       // 16-byte copies of the channels' rows
+  int wide_bc;      // ... and of the rows of b and c
 };
 
-// 2^v; relative error below 2^-22 (flushes results below 2^-126 to zero)
+// 2^v, flushed to zero below 2^-126: relative error below 2^-22.
 __device__ __forceinline__ float exp2_approx(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
+// Two fp32 values in a register pair and the operations on both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The hardware's 2^v is low by 1.8e-8 on average for -0.5 < v < 0 (measured;
+// less than half a step).  Over the hundreds of tokens that a slow state
+// remembers that adds up, so exponents are raised by as much in the same
+// multiply-add that forms them.
+constexpr float EXP_BIAS = 1.8e-8f * 1.4426950408889634f;
+
 __device__ __forceinline__ float step_size(float v, int use_softplus) { return use_softplus ? softplus(v) : v; }
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {  // zeros where not valid
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Copies the tile's W channels (or states) from column col of SCAN_T tokens
+// from t0 on into s [SCAN_T][W], zeros from token `stop` and column `width`
+// (the row's end) on.
+template <typename IO>
+__device__ __forceinline__ void stage_rows(const Rows<IO>& r, int b, int t0, int stop, long long col, long long width, int W,
+                                           bool wide, IO* s) {
+  if (wide) {
+    constexpr int E = 16 / sizeof(IO);
+    const int per = W / E;
+    for (int i = threadIdx.x; i < SCAN_T * per; i += SCAN_W * 32) {
+      const int t = i / per, k = (i - t * per) * E;
+      const bool ok = t0 + t < stop && col + k < width;
+      copy16(s + t * W + k, ok ? r.at(b, t0 + t) + col + k : r.p, ok);
+    }
+  } else {
+    for (int i = threadIdx.x; i < SCAN_T * W; i += SCAN_W * 32) {
+      const int t = i / W, k = i - t * W;
+      s[i] = t0 + t < stop && col + k < width ? r.at(b, t0 + t)[col + k] : from_f<IO>(0.f);
+    }
+  }
+}
+
+// b or c of a tile, [t][n], as fp32 [n][t].
+template <typename IO> __device__ __forceinline__ void transpose_tile(const IO* raw, int N, float* s) {
+  for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
+    const int n = i / SCAN_T, t = i % SCAN_T;
+    s[n * SCAN_LD + t] = to_f<IO>(raw[t * N + n]);
+  }
+}
+
+// What a block works on.
+struct ScanPlace {
+  int b, g, c, chunk, len, tile0, tile1;  // tile1: behind the last tile with tokens
+  long long col;                          // of the block's first channel
+  bool on;                                // whether the lane has a channel
+};
+template <typename IO> __device__ __forceinline__ ScanPlace scan_place(const ScanArgs<IO>& p) {
+  ScanPlace w;
+  const int per = p.C / p.G, lane = threadIdx.x & 31;
+  unsigned i = blockIdx.x;
+  const int blk = i % (p.blocks * p.G);
+  i /= p.blocks * p.G;
+  w.chunk = i % p.chunks;
+  w.b = i / p.chunks;
+  w.g = blk / p.blocks;
+  const int off = (blk % p.blocks) * 32;
+  w.on = off + lane < per;
+  w.col = (long long)w.g * per + off;
+  w.c = (int)w.col + (w.on ? lane : 0);
+  w.len = row_length(p.lengths, w.b, p.T);
+  w.tile0 = w.chunk * p.chunk_tiles;
+  w.tile1 = min(w.tile0 + p.chunk_tiles, (w.len + SCAN_T - 1) / SCAN_T);
+  return w;
+}
+
+// h before the row's first token.  Where rows are cut it comes from the place
+// of the last chunk's end, which nothing needs and where the first pass puts
+// it: state_out may be the same memory as state.
+template <typename IO> __device__ __forceinline__ float scan_first(const ScanArgs<IO>& p, const ScanPlace& w, int n) {
+  return p.state ? p.state[((long long)w.b * p.C + w.c) * p.N + n] : 0.f;
+}
+// h before the block's chunk: the row's first state joined with the chunks before.
+template <typename IO> __device__ __forceinline__ float scan_start(const ScanArgs<IO>& p, const ScanPlace& w, int n, float a) {
+  if (p.chunks == 1) return scan_first(p, w, n);
+  float h = p.ends[(((p.chunks - 1ll) * p.B + w.b) * p.N + n) * p.C + w.c];
+  for (int k = 0; k < w.chunk; ++k) {
+    const long long r = (long long)k * p.B + w.b;
+    h = fmaf(exp2_approx(p.sums[r * p.C + w.c] * a), h, p.ends[(r * p.N + n) * p.C + w.c]);
+  }
+  return h;
+}
+
+enum { SCAN_Y, SCAN_ENDS, SCAN_CKPT };  // y; the chunks' ends and sums; the states before each tile
+
+// Bytes of shared memory, and where its parts lie.
+template <typename IO> struct ScanSmem {
+  IO *x, *dt, *z, *b, *c;  // [slots][T][32 or N]
+  float *de, *dx;          // [2][W][32] float4: delta, delta x
+  float *y;                // [2][W][W][32] float4: sums over a warp's states
+  float *tb, *tc;          // [2][N][LD]
+  float *a, *h;            // [N][32]
+  __host__ __device__ ScanSmem(char* s, int N) {
+    auto take = [&](size_t n) {
+      char* r = s;
+      s += (n + 15) / 16 * 16;
+      return r;
+    };
+    const size_t row = SCAN_SLOTS * SCAN_T * 32 * sizeof(IO), bc = SCAN_SLOTS * SCAN_T * N * sizeof(IO);
+    de = (float*)take(2 * SCAN_T * 32 * 4);
+    dx = (float*)take(2 * SCAN_T * 32 * 4);
+    y = (float*)take(2 * SCAN_W * SCAN_T * 32 * 4);
+    tb = (float*)take(2 * N * SCAN_LD * 4);
+    tc = (float*)take(2 * N * SCAN_LD * 4);
+    a = (float*)take(N * 32 * 4);
+    h = (float*)take(N * 32 * 4);
+    x = (IO*)take(row);
+    dt = (IO*)take(row);
+    z = (IO*)take(row);
+    b = (IO*)take(bc);
+    c = (IO*)take(bc);
+    end = s;
+  }
+  char* end;
+};
+
+// Turn k of the loop copies tile k+2, does C of tile k-1, B of tile k and A of
+// tile k+1: none reads what another of the same turn writes, so one barrier a
+// turn is enough and the warps' phases overlap.
+template <typename IO, int MODE> __global__ void __launch_bounds__(SCAN_W * 32) scan_forward_kernel(const ScanArgs<IO> p) {
+  extern __shared__ __align__(16) char scan_smem[];
+  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const ScanSmem<IO> s(scan_smem, N);
+  const ScanPlace w = scan_place(p);
+  const bool gated = MODE == SCAN_Y && p.z.p;
+  if (MODE == SCAN_ENDS && w.chunk == p.chunks - 1) {  // nothing comes after
+    for (int n = warp; w.on && n < N; n += SCAN_W)
+      p.ends[(((long long)w.chunk * p.B + w.b) * N + n) * p.C + w.c] = scan_first(p, w, n);
+    return;
+  }
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f;
+  const float dskip = MODE == SCAN_Y && p.d ? __ldg(p.d + w.c) : 0.f;
+
+  auto copy = [&](int tile) {
+    if (tile < w.tile1) {
+      const int slot = tile % SCAN_SLOTS, t0 = tile * SCAN_T;
+      stage_rows<IO>(p.x, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.x + slot * SCAN_T * 32);
+      stage_rows<IO>(p.dt, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.dt + slot * SCAN_T * 32);
+      if (gated) stage_rows<IO>(p.z, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.z + slot * SCAN_T * 32);
+      const long long gn = (long long)w.g * N, all = (long long)p.G * N;
+      stage_rows<IO>(p.b, w.b, t0, w.len, gn, all, N, p.wide_bc, s.b + slot * SCAN_T * N);
+      if (MODE == SCAN_Y) stage_rows<IO>(p.c, w.b, t0, w.len, gn, all, N, p.wide_bc, s.c + slot * SCAN_T * N);
+    }
+    copies_commit();
+  };
+  float sum = 0.f;  // of this thread's delta
+  auto phase_a = [&](int tile) {
+    const int slot = tile % SCAN_SLOTS, buf = tile & 1;
+    float de[SCAN_R], dx[SCAN_R];
+#pragma unroll
+    for (int i = 0; i < SCAN_R; ++i) {
+      const int t = warp * SCAN_R + i, at = (slot * SCAN_T + t) * 32 + lane;
+      const float v = step_size(to_f<IO>(s.dt[at]) + bias, p.softplus);
+      de[i] = tile * SCAN_T + t < w.len ? v : 0.f;
+      dx[i] = de[i] * to_f<IO>(s.x[at]);
+      if (MODE == SCAN_ENDS) sum += de[i];
+    }
+    reinterpret_cast<float4*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(de[0], de[1], de[2], de[3]);
+    reinterpret_cast<float4*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(dx[0], dx[1], dx[2], dx[3]);
+    transpose_tile<IO>(s.b + slot * SCAN_T * N, N, s.tb + buf * N * SCAN_LD);
+    if (MODE == SCAN_Y) transpose_tile<IO>(s.c + slot * SCAN_T * N, N, s.tc + buf * N * SCAN_LD);
+  };
+  auto phase_b = [&](int tile) {
+    const int buf = tile & 1;
+    f32x2 de[SCAN_T / 2], dx[SCAN_T / 2], y[SCAN_T / 2];
+#pragma unroll
+    for (int q = 0; q < SCAN_W; ++q) {
+      const ulonglong2 u = reinterpret_cast<const ulonglong2*>(s.de)[(buf * SCAN_W + q) * 32 + lane];
+      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(s.dx)[(buf * SCAN_W + q) * 32 + lane];
+      de[2 * q] = u.x, de[2 * q + 1] = u.y, dx[2 * q] = v.x, dx[2 * q + 1] = v.y;
+      y[2 * q] = y[2 * q + 1] = 0ull;
+    }
+    for (int n = warp; n < N; n += SCAN_W) {
+      const float a = s.a[n * 32 + lane];
+      float h = s.h[n * 32 + lane];
+      if (MODE == SCAN_CKPT && w.on) p.ckpt[(((long long)w.b * p.tiles + tile) * N + n) * p.C + w.c] = h;
+      const f32x2 a2 = pair(a, a), bias2 = pair(EXP_BIAS, EXP_BIAS);
+      const ulonglong2* tb = reinterpret_cast<const ulonglong2*>(s.tb + (buf * N + n) * SCAN_LD);
+      const ulonglong2* tc = reinterpret_cast<const ulonglong2*>(s.tc + (buf * N + n) * SCAN_LD);
+#pragma unroll
+      for (int q = 0; q < SCAN_T / 4; ++q) {
+        const ulonglong2 bq = tb[q];
+        const f32x2 e01 = fma2(de[2 * q], a2, bias2), e23 = fma2(de[2 * q + 1], a2, bias2);
+        const f32x2 b01 = mul2(dx[2 * q], bq.x), b23 = mul2(dx[2 * q + 1], bq.y);
+        float e0, e1, e2, e3, b0, b1, b2, b3;
+        unpair(e01, e0, e1), unpair(e23, e2, e3), unpair(b01, b0, b1), unpair(b23, b2, b3);
+        const float h0 = fmaf(exp2_approx(e0), h, b0), h1 = fmaf(exp2_approx(e1), h0, b1);
+        const float h2 = fmaf(exp2_approx(e2), h1, b2);
+        h = fmaf(exp2_approx(e3), h2, b3);
+        if (MODE == SCAN_Y) {
+          const ulonglong2 cq = tc[q];
+          y[2 * q] = fma2(cq.x, pair(h0, h1), y[2 * q]);
+          y[2 * q + 1] = fma2(cq.y, pair(h2, h), y[2 * q + 1]);
+        }
+      }
+      s.h[n * 32 + lane] = h;
+    }
+    if (MODE == SCAN_Y) {
+#pragma unroll
+      for (int q = 0; q < SCAN_W; ++q)
+        reinterpret_cast<ulonglong2*>(s.y)[((buf * SCAN_W + warp) * SCAN_W + q) * 32 + lane] =
+            make_ulonglong2(y[2 * q], y[2 * q + 1]);
+    }
+  };
+  auto phase_c = [&](int tile) {
+    const int slot = tile % SCAN_SLOTS, buf = tile & 1;
+    float v[SCAN_R] = {};
+#pragma unroll
+    for (int k = 0; k < SCAN_W; ++k) {
+      const float4 u = reinterpret_cast<const float4*>(s.y)[((buf * SCAN_W + k) * SCAN_W + warp) * 32 + lane];
+      v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < SCAN_R; ++i) {
+      const int t = warp * SCAN_R + i, at = (slot * SCAN_T + t) * 32 + lane;
+      v[i] = fmaf(dskip, to_f<IO>(s.x[at]), v[i]);
+      if (gated) {
+        const float z = to_f<IO>(s.z[at]);
+        v[i] *= z * sigmoid(z);
+      }
+      if (w.on && tile * SCAN_T + t < w.len) p.y.at(w.b, tile * SCAN_T + t)[w.c] = from_f<IO>(v[i]);
+    }
+  };
+
+  copy(w.tile0);
+  copy(w.tile0 + 1);
+  for (int n = warp; n < N; n += SCAN_W) {
+    const float a = __ldg(p.a + (long long)w.c * N + n) * LOG2E;
+    s.a[n * 32 + lane] = a;
+    s.h[n * 32 + lane] = MODE == SCAN_ENDS ? 0.f : scan_start(p, w, n, a);
+  }
+  copies_wait<0>();
+  __syncthreads();
+  if (w.tile0 < w.tile1) {
+    phase_a(w.tile0);
+    __syncthreads();
+  }
+  for (int tile = w.tile0; tile < w.tile1; ++tile) {
+    copy(tile + 2);
+    if (MODE == SCAN_Y && tile > w.tile0) phase_c(tile - 1);
+    phase_b(tile);
+    if (tile + 1 < w.tile1) phase_a(tile + 1);
+    copies_wait<0>();
+    __syncthreads();
+  }
+  if constexpr (MODE == SCAN_Y) {
+    if (w.tile0 < w.tile1) phase_c(w.tile1 - 1);
+    if (!w.on) return;
+    const int t1 = min((w.tile0 + p.chunk_tiles) * SCAN_T, p.T);
+    for (int t = max(w.len, w.tile0 * SCAN_T) + warp; t < t1; t += SCAN_W) p.y.at(w.b, t)[w.c] = from_f<IO>(0.f);
+    // the chunk with the row's last token, or the first of an empty row
+    if (p.state_out && w.chunk == max(0, (w.len + SCAN_T - 1) / SCAN_T - 1) / p.chunk_tiles)
+      for (int n = warp; n < N; n += SCAN_W) p.state_out[((long long)w.b * p.C + w.c) * N + n] = s.h[n * 32 + lane];
+  }
+  if constexpr (MODE == SCAN_ENDS) {
+    const long long r = (long long)w.chunk * p.B + w.b;
+    s.y[warp * 32 + lane] = sum;
+    __syncthreads();
+    if (!w.on) return;
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 1; k < SCAN_W; ++k) sum += s.y[k * 32 + lane];
+      p.sums[r * p.C + w.c] = sum;
+    }
+    for (int n = warp; n < N; n += SCAN_W) p.ends[(r * N + n) * p.C + w.c] = s.h[n * 32 + lane];
+  }
+}
 
 // b or c of the tile's tokens as [n][t] floats, zero behind the length.
 template <typename IO>
@@ -53,90 +360,6 @@ __device__ __forceinline__ void scan_load_bc(const Rows<IO>& r, int b, int g, in
   for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
     const int t = i / N, n = i - t * N;
     s[n * SCAN_LD + t] = t0 + t < len ? to_f<IO>(r.at(b, t0 + t)[(long long)g * N + n]) : 0.f;
-  }
-}
-
-// Forward pass; with CKPT, the states before each tile instead of y.
-template <typename IO, bool CKPT> __global__ void __launch_bounds__(SCAN_W * 32) scan_forward_kernel(ScanArgs<IO> p) {
-  extern __shared__ float smem[];
-  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* sd = smem;                        // [T][32] delta
-  float* sx = sd + SCAN_T * 32;            // [T][32] delta x
-  float* sy = sx + SCAN_T * 32;            // [W][T][32] sums over a warp's states
-  float* sb = sy + (CKPT ? 0 : SCAN_W * SCAN_T * 32);  // [N][LD]
-  float* sc = sb + N * SCAN_LD;
-  float* sa = sc + N * SCAN_LD;            // [N][32] a log2(e)
-  float* sh = sa + N * 32;                 // [N][32] h
-  const int per = p.C / p.G;
-  const int blk = blockIdx.x % (p.blocks * p.G), b = blockIdx.x / (p.blocks * p.G);
-  const int g = blk / p.blocks, off = (blk % p.blocks) * 32 + lane;
-  const bool on = off < per;
-  const int c = g * per + (on ? off : 0);
-  const int len = row_length(p.lengths, b, p.T);
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + c) : 0.f, dskip = p.d ? __ldg(p.d + c) : 0.f;
-  for (int n = warp; n < N; n += SCAN_W) {
-    sa[n * 32 + lane] = __ldg(p.a + (long long)c * N + n) * LOG2E;
-    sh[n * 32 + lane] = p.state ? p.state[((long long)b * p.C + c) * N + n] : 0.f;
-  }
-  for (int t0 = 0; t0 < len; t0 += SCAN_T) {
-    float xr[SCAN_R], zr[SCAN_R];
-#pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) {
-      const int t = warp * SCAN_R + i;
-      float delta = 0.f;
-      xr[i] = zr[i] = 0.f;
-      if (on && t0 + t < len) {
-        xr[i] = to_f<IO>(p.x.at(b, t0 + t)[c]);
-        if (!CKPT && p.z.p) zr[i] = to_f<IO>(p.z.at(b, t0 + t)[c]);
-        delta = step_size(to_f<IO>(p.dt.at(b, t0 + t)[c]) + bias, p.softplus);
-      }
-      sd[t * 32 + lane] = delta;
-      sx[t * 32 + lane] = delta * xr[i];
-    }
-    scan_load_bc<IO>(p.b, b, g, t0, len, N, sb);
-    if (!CKPT) scan_load_bc<IO>(p.c, b, g, t0, len, N, sc);
-    __syncthreads();
-    float de[SCAN_T], dx[SCAN_T], y[SCAN_T];
-#pragma unroll
-    for (int t = 0; t < SCAN_T; ++t) {
-      de[t] = sd[t * 32 + lane];
-      dx[t] = sx[t * 32 + lane];
-      y[t] = 0.f;
-    }
-    for (int n = warp; n < N; n += SCAN_W) {
-      const float a = sa[n * 32 + lane];
-      float h = sh[n * 32 + lane];
-      if (CKPT && on) p.ckpt[(((long long)b * p.tiles + t0 / SCAN_T) * N + n) * p.C + c] = h;
-#pragma unroll
-      for (int t = 0; t < SCAN_T; ++t) {
-        h = fmaf(exp2_approx(de[t] * a), h, dx[t] * sb[n * SCAN_LD + t]);
-        if (!CKPT) y[t] = fmaf(sc[n * SCAN_LD + t], h, y[t]);
-      }
-      sh[n * 32 + lane] = h;
-    }
-    if (!CKPT) {
-#pragma unroll
-      for (int t = 0; t < SCAN_T; ++t) sy[(warp * SCAN_T + t) * 32 + lane] = y[t];
-    }
-    __syncthreads();
-    if (!CKPT) {
-#pragma unroll
-      for (int i = 0; i < SCAN_R; ++i) {
-        const int t = warp * SCAN_R + i;
-        if (!on || t0 + t >= len) continue;
-        float v = dskip * xr[i];
-#pragma unroll
-        for (int w = 0; w < SCAN_W; ++w) v += sy[(w * SCAN_T + t) * 32 + lane];
-        if (p.z.p) v *= zr[i] * sigmoid(zr[i]);
-        p.y.at(b, t0 + t)[c] = from_f<IO>(v);
-      }
-    }
-  }
-  if constexpr (!CKPT) {
-    if (!on) return;
-    for (int t = len + warp; t < p.T; t += SCAN_W) p.y.at(b, t)[c] = from_f<IO>(0.f);
-    if (p.state_out)
-      for (int n = warp; n < N; n += SCAN_W) p.state_out[((long long)b * p.C + c) * N + n] = sh[n * 32 + lane];
   }
 }
 

@@ -408,3 +408,16 @@ def test_binding_refusals(cuda_ok):
         wt.norm_forward(x)
     with pytest.raises(wt.WTConvError, match="ARG"):
         wt.norm_backward(x, None, torch.ones(8, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [16, 129, 2000])
+def test_scan_state_updated_in_place(cuda_ok, T):
+    """The state after the pass may take the place of the one before it, also where rows are cut into chunks."""
+    d = cuda(scan_case(2, T, 64, 16, "bf16", seed=8))
+    args = (d["x"], d["dt"], d["a"], d["b"], d["c"], d["d"], d["z"], d["dt_bias"])
+    lengths = torch.tensor([T, T // 3], dtype=torch.int32, device="cuda")
+    y, state = wt.scan_forward(*args, state=d["state"], lengths=lengths)
+    for _ in range(5):
+        s = d["state"].clone()
+        y2, _ = wt.scan_forward(*args, state=s, state_out=s, lengths=lengths)
+        assert torch.equal(y, y2) and torch.equal(s, state)
