@@ -22,7 +22,8 @@ def _files(*dirs):
 
 
 def _deps(src):
-    return _files(os.path.dirname(src), INCLUDE)
+    headers = ["wtconv.h"] + (["wtconv_seq.h"] if os.path.dirname(src) == CSRC_SEQ else [])
+    return _files(os.path.dirname(src)) + [os.path.join(INCLUDE, h) for h in headers]
 
 
 def _object(src):

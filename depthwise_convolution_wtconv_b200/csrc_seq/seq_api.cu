@@ -14,6 +14,7 @@ using namespace wtseq;
 namespace {
 
 constexpr long long MAX_ELEMENTS = 1ll << 56;  // byte offsets stay within 64 bits
+constexpr long long MAX_TOKEN_STRIDE = INT_MAX;  // kernels hold it in 32 bits
 constexpr int SMS = 148;
 
 size_t elt(wtconv_dtype t) { return t == WTCONV_F32 ? 4 : 2; }
@@ -27,7 +28,7 @@ bool dtype_ok(wtconv_dtype t) { return t == WTCONV_F32 || t == WTCONV_BF16; }
 // tokens behind one another within a batch row, or batch rows within a token.
 wtconv_status check_rows(const wtconv_rows* r, size_t e, int B, int T, long long C, bool output) {
   if (!r || !r->data || r->batch_stride < 0 || r->token_stride < 0) return WTCONV_ERR_ARG;
-  if (r->batch_stride > MAX_ELEMENTS / B || r->token_stride > MAX_ELEMENTS / T) return WTCONV_ERR_ARG;
+  if (r->batch_stride > MAX_ELEMENTS / B || (T > 1 && r->token_stride > MAX_TOKEN_STRIDE)) return WTCONV_ERR_ARG;
   if (output) {
     const bool by_row = (T == 1 || r->token_stride >= C) &&
                         (B == 1 || r->batch_stride >= (long long)(T - 1) * r->token_stride + C);
@@ -234,14 +235,25 @@ size_t scan_chunk_floats(const wtconv_scan_desc* d) {
   return chunks == 1 ? 0 : (size_t)chunks * d->B * d->C * (d->N + 1);
 }
 
+// Calls f with the states of a warp: N over the warps, rounded up.
+template <typename F> wtconv_status with_states(int N, F f) {
+  if (N <= 1 * SCAN_W) return f(Int<1>());
+  if (N <= 2 * SCAN_W) return f(Int<2>());
+  if (N <= 4 * SCAN_W) return f(Int<4>());
+  if (N <= 8 * SCAN_W) return f(Int<8>());
+  return f(Int<16>());
+}
+
 template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>& p, cudaStream_t st) {
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
-  const ScanSmem<IO> s(nullptr, p.N);
-  const size_t smem = s.end - (char*)nullptr;
-  TRY(allow_smem(scan_forward_kernel<IO, MODE>, smem));
-  scan_forward_kernel<IO, MODE><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
-  return launched();
+  return with_states(p.N, [&](auto J) {
+    const ScanSmem<IO> s(nullptr, p.N, J.value * SCAN_W);
+    const size_t smem = s.end - (char*)nullptr;
+    TRY((allow_smem(scan_forward_kernel<IO, MODE, J.value>, smem)));
+    scan_forward_kernel<IO, MODE, J.value><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
+    return launched();
+  });
 }
 
 // The chunks' ends where rows are cut, then y or the states before each tile.

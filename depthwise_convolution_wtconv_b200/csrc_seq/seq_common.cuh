@@ -61,34 +61,74 @@ __device__ __forceinline__ int row_length(const int* lengths, int b, int T) {
   return n < 0 ? 0 : (n < T ? n : T);
 }
 
-// 1 / (1 + exp(-v)): exp overflows to infinity for v < -88, and the quotient
-// is then the zero that it should be.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// 2^v and 1/v with results (and arguments) below 2^-126 flushed to zero:
+// relative errors below 2^-22 and 2^-23.  The forms that keep such values cost
+// three more instructions each.
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// 1 / (1 + exp(-v)): the exponential overflows to infinity for v < -88, and
+// the quotient is then the zero that it should be.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + exp2_approx(v * -LOG2E)); }
 
 // d silu(v) / dv, given sigmoid(v)
 __device__ __forceinline__ float dsilu(float v, float sg) { return sg * (1.f + v * (1.f - sg)); }
 
-// log(1 + e) for 0 <= e <= 1 as 2 atanh(s), s = e / (2 + e) <= 1/3, by the
-// Taylor series of atanh: the first term left out is below 2^-25 of the sum.
-// (log(1 + e) from the rounded sum 1 + e would lose the small e, and with
-// them the step sizes near 1e-3 that a scan lives on.)
-__device__ __forceinline__ float log1p_unit(float e) {
-  const float s = __fdividef(e, 2.f + e), q = s * s;
-  float r = 2.f / 15.f;
-  r = fmaf(r, q, 2.f / 13.f);
-  r = fmaf(r, q, 2.f / 11.f);
-  r = fmaf(r, q, 2.f / 9.f);
-  r = fmaf(r, q, 2.f / 7.f);
-  r = fmaf(r, q, 2.f / 5.f);
-  r = fmaf(r, q, 2.f / 3.f);
-  r = fmaf(r, q, 2.f);
-  return s * r;
+// Two fp32 values in a register pair and the operations on both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 twice(float v) { return pair(v, v); }
+__device__ __forceinline__ void unpair(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); NaN stays NaN (v > 0 is then
-// false, and the sum takes it from exp).
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1, of two values.
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, is s times a polynomial in
+// s^2 (degree 4, interpolated at the Chebyshev nodes of [0, 1/9]: off by less
+// than 1e-8).  The logarithm of the rounded sum 1 + e would lose the small e,
+// and with them the step sizes near 1e-3 that a scan lives on.  NaN stays NaN
+// (fmaxf gives 0 then, but the exponential is NaN).
+__device__ __forceinline__ f32x2 softplus2(float v0, float v1) {
+  const float e0 = exp2_approx(fabsf(v0) * -LOG2E), e1 = exp2_approx(fabsf(v1) * -LOG2E);
+  const f32x2 s = pair(e0 * rcp_approx(2.f + e0), e1 * rcp_approx(2.f + e1)), q = mul2(s, s);
+  f32x2 r = fma2(twice(0.28157778f), q, twice(0.27965158f));
+  r = fma2(r, q, twice(0.40024595f));
+  r = fma2(r, q, twice(0.66666322f));
+  r = fma2(r, q, twice(2.f));
+  return fma2(r, s, pair(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+}
 __device__ __forceinline__ float softplus(float v) {
-  return (v > 0.f ? v : 0.f) + log1p_unit(__expf(-fabsf(v)));
+  float a, b;
+  unpair(softplus2(v, v), a, b);
+  return a;
 }
 
 // out[i] = sum over p of part[p * stride + i] in a fixed order: a block holds

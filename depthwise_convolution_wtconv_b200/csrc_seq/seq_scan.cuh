@@ -4,9 +4,9 @@
 // that share out the N states; tokens go by in tiles of SCAN_T.  Per tile:
 //   A  the warps share out the tokens and turn dt and x into delta and
 //      delta x in shared memory, once for all states; b and c go there too;
-//   B  each warp runs the recurrence of its states over the tile with delta
-//      and the sums over its states in registers (state by state, so that the
-//      sums over the states need no exchange between lanes);
+//   B  each warp runs the recurrence of its J states, which live in registers,
+//      four tokens at a time: J independent chains of multiply-adds, and sums
+//      over the warp's states without an exchange between lanes;
 //   C  the warps share out the tokens again, join the warps' sums and apply
 //      d x and the gate.
 // Tokens behind a row's length get delta = 0, x = 0: they leave h as it is.
@@ -26,7 +26,6 @@ constexpr int SCAN_W = 4;         // warps of a block
 constexpr int SCAN_R = SCAN_T / SCAN_W;  // tokens of a warp in A and C: one float4
 constexpr int SCAN_LD = SCAN_T + 4;      // floats between states in the b, c tiles
 constexpr int SCAN_SLOTS = 4;            // tiles of inputs in shared memory
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 static_assert(SCAN_R == 4, "a thread's tokens of a tile are one float4");
 
 template <typename IO> struct ScanArgs {
@@ -51,34 +50,6 @@ template <typename IO> struct ScanArgs {
   int wide_bc;      // ... and of the rows of b and c
 };
 
-// 2^v, flushed to zero below 2^-126: relative error below 2^-22.
-__device__ __forceinline__ float exp2_approx(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// Two fp32 values in a register pair and the operations on both.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(f32x2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // The hardware's 2^v is low by 1.8e-8 on average for -0.5 < v < 0 (measured;
 // less than half a step).  Over the hundreds of tokens that a slow state
 // remembers that adds up, so exponents are raised by as much in the same
@@ -97,33 +68,79 @@ template <int PENDING> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// Copies the tile's W channels (or states) from column col of SCAN_T tokens
-// from t0 on into s [SCAN_T][W], zeros from token `stop` and column `width`
-// (the row's end) on.
-template <typename IO>
-__device__ __forceinline__ void stage_rows(const Rows<IO>& r, int b, int t0, int stop, long long col, long long width, int W,
-                                           bool wide, IO* s) {
-  if (wide) {
-    constexpr int E = 16 / sizeof(IO);
-    const int per = W / E;
-    for (int i = threadIdx.x; i < SCAN_T * per; i += SCAN_W * 32) {
-      const int t = i / per, k = (i - t * per) * E;
-      const bool ok = t0 + t < stop && col + k < width;
-      copy16(s + t * W + k, ok ? r.at(b, t0 + t) + col + k : r.p, ok);
+// One warp's copies of a tile of 32 channels, [SCAN_T][32], tile by tile: 16
+// bytes a lane where the rows suit that, with pointers that only move on.
+// Tokens from `stop` on and columns from `width` on become zeros.
+template <typename IO> struct RowCopy {
+  static constexpr int E = 16 / sizeof(IO), PER = 32 / E, ROWS = 32 / PER;  // elements, chunks a row, rows a pass
+  const IO* p;
+  int row, st;
+  bool ok;
+  __device__ __forceinline__ RowCopy(const Rows<IO>& r, int b, int tile, long long col, long long width, bool wide) {
+    const int lane = threadIdx.x & 31, k = wide ? lane % PER * E : lane;
+    row = tile * SCAN_T + (wide ? lane / PER : 0);
+    st = (int)r.st;
+    ok = col + k < width;
+    p = r.at(b, row) + (ok ? col + k : 0);
+  }
+  __device__ __forceinline__ void tile(bool wide, int stop, IO* s) {
+    const int lane = threadIdx.x & 31;
+    if (wide) {
+      IO* d = s + (lane / PER) * 32 + lane % PER * E;
+#pragma unroll
+      for (int k = 0; k < SCAN_T; k += ROWS) copy16(d + k * 32, p + (long long)k * st, ok && row + k < stop);
+    } else {
+#pragma unroll 4
+      for (int k = 0; k < SCAN_T; ++k) s[k * 32 + lane] = ok && row + k < stop ? p[(long long)k * st] : from_f<IO>(0.f);
     }
-  } else {
-    for (int i = threadIdx.x; i < SCAN_T * W; i += SCAN_W * 32) {
-      const int t = i / W, k = i - t * W;
-      s[i] = t0 + t < stop && col + k < width ? r.at(b, t0 + t)[col + k] : from_f<IO>(0.f);
+    row += SCAN_T;
+    p += (long long)SCAN_T * st;
+  }
+};
+// One warp's copies of tiles of b and c, [SCAN_T][N].
+template <typename IO> struct StateCopy {
+  static constexpr int E = 16 / sizeof(IO);
+  int per, t, k, step;  // chunks a row; the lane's first token and state, tokens a pass (0: no whole number)
+  __device__ __forceinline__ StateCopy(int N, bool wide) {
+    const int lane = threadIdx.x & 31, e = wide ? E : 1;
+    per = N / e;
+    t = lane / per;
+    k = (lane - t * per) * e;
+    step = 32 % per ? 0 : 32 / per;
+  }
+  __device__ __forceinline__ void one(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide, int t, int k,
+                                      IO* s) const {
+    const bool ok = t0 + t < stop;
+    const IO* p = ok ? r.at(b, t0 + t) + col + k : r.p;
+    if (wide)
+      copy16(s + t * N + k, p, ok);
+    else
+      s[t * N + k] = ok ? *p : from_f<IO>(0.f);
+  }
+  __device__ __forceinline__ void tile(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide, IO* s) const {
+    if (step) {
+      for (int u = t; u < SCAN_T; u += step) one(r, b, t0, stop, col, N, wide, u, k, s);
+    } else {
+      for (int i = threadIdx.x & 31; i < SCAN_T * per; i += 32)
+        one(r, b, t0, stop, col, N, wide, i / per, i % per * (wide ? E : 1), s);
     }
   }
-}
+};
 
 // b or c of a tile, [t][n], as fp32 [n][t].
 template <typename IO> __device__ __forceinline__ void transpose_tile(const IO* raw, int N, float* s) {
-  for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
-    const int n = i / SCAN_T, t = i % SCAN_T;
-    s[n * SCAN_LD + t] = to_f<IO>(raw[t * N + n]);
+  if (N & 1) {
+    for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
+      const int n = i / SCAN_T, t = i % SCAN_T;
+      s[n * SCAN_LD + t] = to_f<IO>(raw[t * N + n]);
+    }
+  } else {
+    for (int i = threadIdx.x; i < SCAN_T * N / 2; i += SCAN_W * 32) {
+      const int n = i / SCAN_T * 2, t = i % SCAN_T;
+      const Pack<IO, 2> v = *reinterpret_cast<const Pack<IO, 2>*>(raw + t * N + n);
+      s[n * SCAN_LD + t] = to_f<IO>(v.v[0]);
+      s[(n + 1) * SCAN_LD + t] = to_f<IO>(v.v[1]);
+    }
   }
 }
 
@@ -176,9 +193,8 @@ template <typename IO> struct ScanSmem {
   IO *x, *dt, *z, *b, *c;  // [slots][T][32 or N]
   float *de, *dx;          // [2][W][32] float4: delta, delta x
   float *y;                // [2][W][W][32] float4: sums over a warp's states
-  float *tb, *tc;          // [2][N][LD]
-  float *a, *h;            // [N][32]
-  __host__ __device__ ScanSmem(char* s, int N) {
+  float *tb, *tc;          // [2][NP][LD], NP: N rounded up to the warps' states
+  __host__ __device__ ScanSmem(char* s, int N, int NP) {
     auto take = [&](size_t n) {
       char* r = s;
       s += (n + 15) / 16 * 16;
@@ -188,10 +204,8 @@ template <typename IO> struct ScanSmem {
     de = (float*)take(2 * SCAN_T * 32 * 4);
     dx = (float*)take(2 * SCAN_T * 32 * 4);
     y = (float*)take(2 * SCAN_W * SCAN_T * 32 * 4);
-    tb = (float*)take(2 * N * SCAN_LD * 4);
-    tc = (float*)take(2 * N * SCAN_LD * 4);
-    a = (float*)take(N * 32 * 4);
-    h = (float*)take(N * 32 * 4);
+    tb = (float*)take(2 * NP * SCAN_LD * 4);
+    tc = (float*)take(2 * NP * SCAN_LD * 4);
     x = (IO*)take(row);
     dt = (IO*)take(row);
     z = (IO*)take(row);
@@ -205,10 +219,12 @@ template <typename IO> struct ScanSmem {
 // Turn k of the loop copies tile k+2, does C of tile k-1, B of tile k and A of
 // tile k+1: none reads what another of the same turn writes, so one barrier a
 // turn is enough and the warps' phases overlap.
-template <typename IO, int MODE> __global__ void __launch_bounds__(SCAN_W * 32) scan_forward_kernel(const ScanArgs<IO> p) {
+template <typename IO, int MODE, int J>
+__global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 6 : (J <= 8 ? 4 : 2)) scan_forward_kernel(const ScanArgs<IO> p) {
   extern __shared__ __align__(16) char scan_smem[];
-  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const ScanSmem<IO> s(scan_smem, N);
+  constexpr int NP = J * SCAN_W;
+  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
+  const ScanSmem<IO> s(scan_smem, N, NP);
   const ScanPlace w = scan_place(p);
   const bool gated = MODE == SCAN_Y && p.z.p;
   if (MODE == SCAN_ENDS && w.chunk == p.chunks - 1) {  // nothing comes after
@@ -219,103 +235,118 @@ template <typename IO, int MODE> __global__ void __launch_bounds__(SCAN_W * 32) 
   const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f;
   const float dskip = MODE == SCAN_Y && p.d ? __ldg(p.d + w.c) : 0.f;
 
-  auto copy = [&](int tile) {
+  // warp 0 copies x, 1 dt, 2 z, 3 b and c; SCAN_T tokens by 32 channels each
+  static_assert(SCAN_W == 4, "a warp for each input");
+  RowCopy<IO> rows(warp == 0 || !gated && warp == 2 ? p.x : (warp == 2 ? p.z : p.dt), w.b, w.tile0, w.col, p.C, p.wide_x);
+  const StateCopy<IO> states(N, p.wide_bc);
+  IO* const raw = warp == 0 ? s.x : (warp == 1 ? s.dt : s.z);
+  auto copy = [&](int tile) {  // in order
     if (tile < w.tile1) {
       const int slot = tile % SCAN_SLOTS, t0 = tile * SCAN_T;
-      stage_rows<IO>(p.x, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.x + slot * SCAN_T * 32);
-      stage_rows<IO>(p.dt, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.dt + slot * SCAN_T * 32);
-      if (gated) stage_rows<IO>(p.z, w.b, t0, w.len, w.col, p.C, 32, p.wide_x, s.z + slot * SCAN_T * 32);
-      const long long gn = (long long)w.g * N, all = (long long)p.G * N;
-      stage_rows<IO>(p.b, w.b, t0, w.len, gn, all, N, p.wide_bc, s.b + slot * SCAN_T * N);
-      if (MODE == SCAN_Y) stage_rows<IO>(p.c, w.b, t0, w.len, gn, all, N, p.wide_bc, s.c + slot * SCAN_T * N);
+      if (warp < 2 || warp == 2 && gated) {
+        rows.tile(p.wide_x, w.len, raw + slot * SCAN_T * 32);
+      } else if (warp == 3) {
+        states.tile(p.b, w.b, t0, w.len, (long long)w.g * N, N, p.wide_bc, s.b + slot * SCAN_T * N);
+        if (MODE == SCAN_Y) states.tile(p.c, w.b, t0, w.len, (long long)w.g * N, N, p.wide_bc, s.c + slot * SCAN_T * N);
+      }
     }
     copies_commit();
   };
   float sum = 0.f;  // of this thread's delta
   auto phase_a = [&](int tile) {
     const int slot = tile % SCAN_SLOTS, buf = tile & 1;
-    float de[SCAN_R], dx[SCAN_R];
+    f32x2 de[SCAN_R / 2], dx[SCAN_R / 2];
 #pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) {
-      const int t = warp * SCAN_R + i, at = (slot * SCAN_T + t) * 32 + lane;
-      const float v = step_size(to_f<IO>(s.dt[at]) + bias, p.softplus);
-      de[i] = tile * SCAN_T + t < w.len ? v : 0.f;
-      dx[i] = de[i] * to_f<IO>(s.x[at]);
-      if (MODE == SCAN_ENDS) sum += de[i];
+    for (int i = 0; i < SCAN_R / 2; ++i) {
+      const int t = warp * SCAN_R + 2 * i, at = (slot * SCAN_T + t) * 32 + lane;
+      const float v0 = to_f<IO>(s.dt[at]) + bias, v1 = to_f<IO>(s.dt[at + 32]) + bias;
+      float d0 = v0, d1 = v1;
+      if (p.softplus) unpair(softplus2(v0, v1), d0, d1);
+      if (tile * SCAN_T + t >= w.len) d0 = 0.f;
+      if (tile * SCAN_T + t + 1 >= w.len) d1 = 0.f;
+      if (MODE == SCAN_ENDS) sum += d0 + d1;
+      de[i] = pair(d0, d1);
+      dx[i] = mul2(de[i], pair(to_f<IO>(s.x[at]), to_f<IO>(s.x[at + 32])));
     }
-    reinterpret_cast<float4*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(de[0], de[1], de[2], de[3]);
-    reinterpret_cast<float4*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(dx[0], dx[1], dx[2], dx[3]);
-    transpose_tile<IO>(s.b + slot * SCAN_T * N, N, s.tb + buf * N * SCAN_LD);
-    if (MODE == SCAN_Y) transpose_tile<IO>(s.c + slot * SCAN_T * N, N, s.tc + buf * N * SCAN_LD);
+    reinterpret_cast<ulonglong2*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_ulonglong2(de[0], de[1]);
+    reinterpret_cast<ulonglong2*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] = make_ulonglong2(dx[0], dx[1]);
+    transpose_tile<IO>(s.b + slot * SCAN_T * N, N, s.tb + buf * NP * SCAN_LD);
+    if (MODE == SCAN_Y) transpose_tile<IO>(s.c + slot * SCAN_T * N, N, s.tc + buf * NP * SCAN_LD);
   };
+  f32x2 a2[J];  // a log2(e), twice
+  float h[J];
+  const f32x2 bias2 = twice(EXP_BIAS);
   auto phase_b = [&](int tile) {
     const int buf = tile & 1;
-    f32x2 de[SCAN_T / 2], dx[SCAN_T / 2], y[SCAN_T / 2];
+    if (MODE == SCAN_CKPT && w.on) {
+      float* k = p.ckpt + (((long long)w.b * p.tiles + tile) * N + n0) * p.C + w.c;
 #pragma unroll
-    for (int q = 0; q < SCAN_W; ++q) {
-      const ulonglong2 u = reinterpret_cast<const ulonglong2*>(s.de)[(buf * SCAN_W + q) * 32 + lane];
-      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(s.dx)[(buf * SCAN_W + q) * 32 + lane];
-      de[2 * q] = u.x, de[2 * q + 1] = u.y, dx[2 * q] = v.x, dx[2 * q + 1] = v.y;
-      y[2 * q] = y[2 * q + 1] = 0ull;
+      for (int j = 0; j < J; ++j)
+        if (n0 + j < N) k[(long long)j * p.C] = h[j];
     }
-    for (int n = warp; n < N; n += SCAN_W) {
-      const float a = s.a[n * 32 + lane];
-      float h = s.h[n * 32 + lane];
-      if (MODE == SCAN_CKPT && w.on) p.ckpt[(((long long)w.b * p.tiles + tile) * N + n) * p.C + w.c] = h;
-      const f32x2 a2 = pair(a, a), bias2 = pair(EXP_BIAS, EXP_BIAS);
-      const ulonglong2* tb = reinterpret_cast<const ulonglong2*>(s.tb + (buf * N + n) * SCAN_LD);
-      const ulonglong2* tc = reinterpret_cast<const ulonglong2*>(s.tc + (buf * N + n) * SCAN_LD);
+    const ulonglong2* de = reinterpret_cast<const ulonglong2*>(s.de) + buf * SCAN_W * 32 + lane;
+    const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + buf * SCAN_W * 32 + lane;
+    const float* tb = s.tb + (buf * NP + n0) * SCAN_LD;
+    const float* tc = s.tc + (buf * NP + n0) * SCAN_LD;
 #pragma unroll
-      for (int q = 0; q < SCAN_T / 4; ++q) {
-        const ulonglong2 bq = tb[q];
-        const f32x2 e01 = fma2(de[2 * q], a2, bias2), e23 = fma2(de[2 * q + 1], a2, bias2);
-        const f32x2 b01 = mul2(dx[2 * q], bq.x), b23 = mul2(dx[2 * q + 1], bq.y);
+    for (int q = 0; q < SCAN_T / 4; ++q) {
+      const ulonglong2 d = de[q * 32], u = dx[q * 32];
+      f32x2 y01 = 0, y23 = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(tb + j * SCAN_LD + 4 * q);
+        const f32x2 e01 = fma2(d.x, a2[j], bias2), e23 = fma2(d.y, a2[j], bias2);
+        const f32x2 b01 = mul2(u.x, bq.x), b23 = mul2(u.y, bq.y);
         float e0, e1, e2, e3, b0, b1, b2, b3;
         unpair(e01, e0, e1), unpair(e23, e2, e3), unpair(b01, b0, b1), unpair(b23, b2, b3);
-        const float h0 = fmaf(exp2_approx(e0), h, b0), h1 = fmaf(exp2_approx(e1), h0, b1);
+        const float h0 = fmaf(exp2_approx(e0), h[j], b0), h1 = fmaf(exp2_approx(e1), h0, b1);
         const float h2 = fmaf(exp2_approx(e2), h1, b2);
-        h = fmaf(exp2_approx(e3), h2, b3);
+        h[j] = fmaf(exp2_approx(e3), h2, b3);
         if (MODE == SCAN_Y) {
-          const ulonglong2 cq = tc[q];
-          y[2 * q] = fma2(cq.x, pair(h0, h1), y[2 * q]);
-          y[2 * q + 1] = fma2(cq.y, pair(h2, h), y[2 * q + 1]);
+          const ulonglong2 cq = *reinterpret_cast<const ulonglong2*>(tc + j * SCAN_LD + 4 * q);
+          y01 = fma2(cq.x, pair(h0, h1), y01);
+          y23 = fma2(cq.y, pair(h2, h[j]), y23);
         }
       }
-      s.h[n * 32 + lane] = h;
-    }
-    if (MODE == SCAN_Y) {
-#pragma unroll
-      for (int q = 0; q < SCAN_W; ++q)
-        reinterpret_cast<ulonglong2*>(s.y)[((buf * SCAN_W + warp) * SCAN_W + q) * 32 + lane] =
-            make_ulonglong2(y[2 * q], y[2 * q + 1]);
+      if (MODE == SCAN_Y)
+        reinterpret_cast<ulonglong2*>(s.y)[((buf * SCAN_W + warp) * SCAN_W + q) * 32 + lane] = make_ulonglong2(y01, y23);
     }
   };
   auto phase_c = [&](int tile) {
     const int slot = tile % SCAN_SLOTS, buf = tile & 1;
-    float v[SCAN_R] = {};
+    f32x2 u[SCAN_R / 2] = {};
 #pragma unroll
     for (int k = 0; k < SCAN_W; ++k) {
-      const float4 u = reinterpret_cast<const float4*>(s.y)[((buf * SCAN_W + k) * SCAN_W + warp) * 32 + lane];
-      v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(s.y)[((buf * SCAN_W + k) * SCAN_W + warp) * 32 + lane];
+      u[0] = add2(u[0], v.x), u[1] = add2(u[1], v.y);
     }
+    float v[SCAN_R];
+    unpair(u[0], v[0], v[1]), unpair(u[1], v[2], v[3]);
+    IO* out = p.y.at(w.b, tile * SCAN_T + warp * SCAN_R) + w.c;
+    const int left = w.on ? w.len - (tile * SCAN_T + warp * SCAN_R) : 0, st = (int)p.y.st;
 #pragma unroll
     for (int i = 0; i < SCAN_R; ++i) {
-      const int t = warp * SCAN_R + i, at = (slot * SCAN_T + t) * 32 + lane;
+      const int at = (slot * SCAN_T + warp * SCAN_R + i) * 32 + lane;
       v[i] = fmaf(dskip, to_f<IO>(s.x[at]), v[i]);
       if (gated) {
         const float z = to_f<IO>(s.z[at]);
         v[i] *= z * sigmoid(z);
       }
-      if (w.on && tile * SCAN_T + t < w.len) p.y.at(w.b, tile * SCAN_T + t)[w.c] = from_f<IO>(v[i]);
+      if (i < left) out[(long long)i * st] = from_f<IO>(v[i]);
     }
   };
 
   copy(w.tile0);
   copy(w.tile0 + 1);
-  for (int n = warp; n < N; n += SCAN_W) {
-    const float a = __ldg(p.a + (long long)w.c * N + n) * LOG2E;
-    s.a[n * 32 + lane] = a;
-    s.h[n * 32 + lane] = MODE == SCAN_ENDS ? 0.f : scan_start(p, w, n, a);
+  for (int i = threadIdx.x; i < 2 * (NP - N) * SCAN_LD; i += SCAN_W * 32) {  // states that are not there
+    const int k = i / ((NP - N) * SCAN_LD), r = i % ((NP - N) * SCAN_LD) + (k * NP + N) * SCAN_LD;
+    s.tb[r] = s.tc[r] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float a = n0 + j < N ? __ldg(p.a + (long long)w.c * N + n0 + j) * LOG2E : 0.f;
+    a2[j] = twice(a);
+    h[j] = MODE == SCAN_ENDS || n0 + j >= N ? 0.f : scan_start(p, w, n0 + j, a);
   }
   copies_wait<0>();
   __syncthreads();
@@ -338,7 +369,9 @@ template <typename IO, int MODE> __global__ void __launch_bounds__(SCAN_W * 32) 
     for (int t = max(w.len, w.tile0 * SCAN_T) + warp; t < t1; t += SCAN_W) p.y.at(w.b, t)[w.c] = from_f<IO>(0.f);
     // the chunk with the row's last token, or the first of an empty row
     if (p.state_out && w.chunk == max(0, (w.len + SCAN_T - 1) / SCAN_T - 1) / p.chunk_tiles)
-      for (int n = warp; n < N; n += SCAN_W) p.state_out[((long long)w.b * p.C + w.c) * N + n] = s.h[n * 32 + lane];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (n0 + j < N) p.state_out[((long long)w.b * p.C + w.c) * N + n0 + j] = h[j];
   }
   if constexpr (MODE == SCAN_ENDS) {
     const long long r = (long long)w.chunk * p.B + w.b;
@@ -350,7 +383,9 @@ template <typename IO, int MODE> __global__ void __launch_bounds__(SCAN_W * 32) 
       for (int k = 1; k < SCAN_W; ++k) sum += s.y[k * 32 + lane];
       p.sums[r * p.C + w.c] = sum;
     }
-    for (int n = warp; n < N; n += SCAN_W) p.ends[(r * N + n) * p.C + w.c] = s.h[n * 32 + lane];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (n0 + j < N) p.ends[(r * N + n0 + j) * p.C + w.c] = h[j];
   }
 }
 

@@ -68,7 +68,8 @@ extern "C" {
 #define WTCONV_NORM_MAX_C 16384
 
 /* Rows of an activation: channel c of token t of batch row b is
- * data[b * batch_stride + t * token_stride + c], strides in elements. */
+ * data[b * batch_stride + t * token_stride + c], strides in elements (the
+ * token stride at most 2^31 - 1). */
 typedef struct {
   void* data;
   long long batch_stride, token_stride;
