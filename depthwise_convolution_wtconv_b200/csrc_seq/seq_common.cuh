@@ -110,25 +110,20 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1, of two values.
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1.
 // log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, is s times a polynomial in
 // s^2 (degree 4, interpolated at the Chebyshev nodes of [0, 1/9]: off by less
 // than 1e-8).  The logarithm of the rounded sum 1 + e would lose the small e,
 // and with them the step sizes near 1e-3 that a scan lives on.  NaN stays NaN
 // (fmaxf gives 0 then, but the exponential is NaN).
-__device__ __forceinline__ f32x2 softplus2(float v0, float v1) {
-  const float e0 = exp2_approx(fabsf(v0) * -LOG2E), e1 = exp2_approx(fabsf(v1) * -LOG2E);
-  const f32x2 s = pair(e0 * rcp_approx(2.f + e0), e1 * rcp_approx(2.f + e1)), q = mul2(s, s);
-  f32x2 r = fma2(twice(0.28157778f), q, twice(0.27965158f));
-  r = fma2(r, q, twice(0.40024595f));
-  r = fma2(r, q, twice(0.66666322f));
-  r = fma2(r, q, twice(2.f));
-  return fma2(r, s, pair(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
-}
 __device__ __forceinline__ float softplus(float v) {
-  float a, b;
-  unpair(softplus2(v, v), a, b);
-  return a;
+  const float e = exp2_approx(fabsf(v) * -LOG2E);
+  const float s = e * rcp_approx(2.f + e), q = s * s;
+  float r = fmaf(0.28157778f, q, 0.27965158f);
+  r = fmaf(r, q, 0.40024595f);
+  r = fmaf(r, q, 0.66666322f);
+  r = fmaf(r, q, 2.f);
+  return fmaf(r, s, fmaxf(v, 0.f));
 }
 
 // out[i] = sum over p of part[p * stride + i] in a fixed order: a block holds

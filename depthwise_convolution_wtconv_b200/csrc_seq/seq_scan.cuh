@@ -68,78 +68,84 @@ template <int PENDING> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// One warp's copies of a tile of 32 channels, [SCAN_T][32], tile by tile: 16
-// bytes a lane where the rows suit that, with pointers that only move on.
-// Tokens from `stop` on and columns from `width` on become zeros.
-template <typename IO> struct RowCopy {
+// A lane's share of the copies of one input, tile by tile, 16 bytes at a time
+// where the rows suit that: pointers that only move on.  Tokens behind the
+// length become zeros.  `wide` decides between the two forms below.
+template <typename IO> struct RowCopy {  // [SCAN_T][32 channels]
   static constexpr int E = 16 / sizeof(IO), PER = 32 / E, ROWS = 32 / PER;  // elements, chunks a row, rows a pass
   const IO* p;
-  int row, st;
-  bool ok;
-  __device__ __forceinline__ RowCopy(const Rows<IO>& r, int b, int tile, long long col, long long width, bool wide) {
-    const int lane = threadIdx.x & 31, k = wide ? lane % PER * E : lane;
-    row = tile * SCAN_T + (wide ? lane / PER : 0);
+  int left, st, at;  // tokens left from the lane's first one on (none for a lane outside the channels)
+  __device__ __forceinline__ RowCopy(const Rows<IO>& r, int b, int t0, int stop, long long col, long long width, bool wide) {
+    const int lane = threadIdx.x & 31, t = wide ? lane / PER : 0, k = wide ? lane % PER * E : lane;
+    const bool ok = col + k < width;
+    p = r.at(b, t0 + t) + (ok ? col + k : 0);
+    left = ok ? stop - t0 - t : 0;
     st = (int)r.st;
-    ok = col + k < width;
-    p = r.at(b, row) + (ok ? col + k : 0);
+    at = t * 32 + k;
   }
-  __device__ __forceinline__ void tile(bool wide, int stop, IO* s) {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ void tile(bool wide, IO* s) {
     if (wide) {
-      IO* d = s + (lane / PER) * 32 + lane % PER * E;
 #pragma unroll
-      for (int k = 0; k < SCAN_T; k += ROWS) copy16(d + k * 32, p + (long long)k * st, ok && row + k < stop);
+      for (int k = 0; k < SCAN_T; k += ROWS) copy16(s + at + k * 32, p + (long long)k * st, k < left);
     } else {
 #pragma unroll 4
-      for (int k = 0; k < SCAN_T; ++k) s[k * 32 + lane] = ok && row + k < stop ? p[(long long)k * st] : from_f<IO>(0.f);
+      for (int k = 0; k < SCAN_T; ++k) s[at + k * 32] = k < left ? p[(long long)k * st] : from_f<IO>(0.f);
     }
-    row += SCAN_T;
+    left -= SCAN_T;
     p += (long long)SCAN_T * st;
   }
 };
-// One warp's copies of tiles of b and c, [SCAN_T][N].
-template <typename IO> struct StateCopy {
+template <typename IO> struct StateCopy {  // [SCAN_T][N states]
   static constexpr int E = 16 / sizeof(IO);
-  int per, t, k, step;  // chunks a row; the lane's first token and state, tokens a pass (0: no whole number)
-  __device__ __forceinline__ StateCopy(int N, bool wide) {
+  const IO* p;
+  int left, st, per, t, step;  // tokens left; chunks a row; the lane's first token, tokens a pass (0: not a whole number)
+  __device__ __forceinline__ StateCopy(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide) {
     const int lane = threadIdx.x & 31, e = wide ? E : 1;
     per = N / e;
     t = lane / per;
-    k = (lane - t * per) * e;
     step = 32 % per ? 0 : 32 / per;
+    p = r.at(b, t0) + col;
+    left = stop - t0;
+    st = (int)r.st;
   }
-  __device__ __forceinline__ void one(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide, int t, int k,
-                                      IO* s) const {
-    const bool ok = t0 + t < stop;
-    const IO* p = ok ? r.at(b, t0 + t) + col + k : r.p;
+  __device__ __forceinline__ void one(int t, int k, bool wide, int N, IO* s) const {
     if (wide)
-      copy16(s + t * N + k, p, ok);
+      copy16(s + t * N + k, p + (long long)t * st + k, t < left);
     else
-      s[t * N + k] = ok ? *p : from_f<IO>(0.f);
+      s[t * N + k] = t < left ? p[(long long)t * st + k] : from_f<IO>(0.f);
   }
-  __device__ __forceinline__ void tile(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide, IO* s) const {
+  __device__ __forceinline__ void tile(bool wide, int N, IO* s) {
+    const int lane = threadIdx.x & 31, e = wide ? E : 1;
     if (step) {
-      for (int u = t; u < SCAN_T; u += step) one(r, b, t0, stop, col, N, wide, u, k, s);
+      const int k = (lane - t * per) * e;
+      for (int u = t; u < SCAN_T; u += step) one(u, k, wide, N, s);
     } else {
-      for (int i = threadIdx.x & 31; i < SCAN_T * per; i += 32)
-        one(r, b, t0, stop, col, N, wide, i / per, i % per * (wide ? E : 1), s);
+      for (int i = lane; i < SCAN_T * per; i += 32) one(i / per, i % per * e, wide, N, s);
     }
+    left -= SCAN_T;
+    p += (long long)SCAN_T * st;
   }
 };
 
-// b or c of a tile, [t][n], as fp32 [n][t].
-template <typename IO> __device__ __forceinline__ void transpose_tile(const IO* raw, int N, float* s) {
+// b and c of a tile, [t][n], as fp32 [n][t]: a thread per token and two states.
+template <typename IO, bool BOTH>
+__device__ __forceinline__ void transpose_tiles(const IO* b, const IO* c, int N, float* tb, float* tc) {
+  const int t = threadIdx.x % SCAN_T;
   if (N & 1) {
-    for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
-      const int n = i / SCAN_T, t = i % SCAN_T;
-      s[n * SCAN_LD + t] = to_f<IO>(raw[t * N + n]);
+    for (int n = threadIdx.x / SCAN_T; n < N; n += SCAN_W * 32 / SCAN_T) {
+      tb[n * SCAN_LD + t] = to_f<IO>(b[t * N + n]);
+      if (BOTH) tc[n * SCAN_LD + t] = to_f<IO>(c[t * N + n]);
     }
-  } else {
-    for (int i = threadIdx.x; i < SCAN_T * N / 2; i += SCAN_W * 32) {
-      const int n = i / SCAN_T * 2, t = i % SCAN_T;
-      const Pack<IO, 2> v = *reinterpret_cast<const Pack<IO, 2>*>(raw + t * N + n);
-      s[n * SCAN_LD + t] = to_f<IO>(v.v[0]);
-      s[(n + 1) * SCAN_LD + t] = to_f<IO>(v.v[1]);
+    return;
+  }
+  for (int n = threadIdx.x / SCAN_T * 2; n < N; n += SCAN_W * 64 / SCAN_T) {
+    const Pack<IO, 2> u = *reinterpret_cast<const Pack<IO, 2>*>(b + t * N + n);
+    tb[n * SCAN_LD + t] = to_f<IO>(u.v[0]);
+    tb[(n + 1) * SCAN_LD + t] = to_f<IO>(u.v[1]);
+    if (BOTH) {
+      const Pack<IO, 2> v = *reinterpret_cast<const Pack<IO, 2>*>(c + t * N + n);
+      tc[n * SCAN_LD + t] = to_f<IO>(v.v[0]);
+      tc[(n + 1) * SCAN_LD + t] = to_f<IO>(v.v[1]);
     }
   }
 }
@@ -220,7 +226,7 @@ template <typename IO> struct ScanSmem {
 // tile k+1: none reads what another of the same turn writes, so one barrier a
 // turn is enough and the warps' phases overlap.
 template <typename IO, int MODE, int J>
-__global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 6 : (J <= 8 ? 4 : 2)) scan_forward_kernel(const ScanArgs<IO> p) {
+__global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) scan_forward_kernel(const ScanArgs<IO> p) {
   extern __shared__ __align__(16) char scan_smem[];
   constexpr int NP = J * SCAN_W;
   const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
@@ -235,54 +241,61 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 6 : (J <= 8 ? 4 : 2)) sc
   const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f;
   const float dskip = MODE == SCAN_Y && p.d ? __ldg(p.d + w.c) : 0.f;
 
-  // warp 0 copies x, 1 dt, 2 z, 3 b and c; SCAN_T tokens by 32 channels each
+  // warp 0 copies x, 1 dt, 2 z, 3 b and c
   static_assert(SCAN_W == 4, "a warp for each input");
-  RowCopy<IO> rows(warp == 0 || !gated && warp == 2 ? p.x : (warp == 2 ? p.z : p.dt), w.b, w.tile0, w.col, p.C, p.wide_x);
-  const StateCopy<IO> states(N, p.wide_bc);
+  const int first = w.tile0 * SCAN_T, count = max(0, w.tile1 - w.tile0);
+  RowCopy<IO> rows(warp == 2 && gated ? p.z : (warp == 1 ? p.dt : p.x), w.b, first, w.len, w.col, p.C, p.wide_x);
+  StateCopy<IO> rows_b(p.b, w.b, first, w.len, (long long)w.g * N, N, p.wide_bc);
+  StateCopy<IO> rows_c(p.c, w.b, first, w.len, (long long)w.g * N, N, p.wide_bc);
   IO* const raw = warp == 0 ? s.x : (warp == 1 ? s.dt : s.z);
-  auto copy = [&](int tile) {  // in order
-    if (tile < w.tile1) {
-      const int slot = tile % SCAN_SLOTS, t0 = tile * SCAN_T;
+  // the phases count tiles from the block's first; copies go in order
+  auto copy = [&](int k) {
+    if (k < count) {
+      const int slot = k % SCAN_SLOTS;
       if (warp < 2 || warp == 2 && gated) {
-        rows.tile(p.wide_x, w.len, raw + slot * SCAN_T * 32);
+        rows.tile(p.wide_x, raw + slot * (SCAN_T * 32));
       } else if (warp == 3) {
-        states.tile(p.b, w.b, t0, w.len, (long long)w.g * N, N, p.wide_bc, s.b + slot * SCAN_T * N);
-        if (MODE == SCAN_Y) states.tile(p.c, w.b, t0, w.len, (long long)w.g * N, N, p.wide_bc, s.c + slot * SCAN_T * N);
+        rows_b.tile(p.wide_bc, N, s.b + slot * SCAN_T * N);
+        if (MODE == SCAN_Y) rows_c.tile(p.wide_bc, N, s.c + slot * SCAN_T * N);
       }
     }
     copies_commit();
   };
   float sum = 0.f;  // of this thread's delta
-  auto phase_a = [&](int tile) {
-    const int slot = tile % SCAN_SLOTS, buf = tile & 1;
-    f32x2 de[SCAN_R / 2], dx[SCAN_R / 2];
+  const int mine = w.len - first - warp * SCAN_R;  // tokens from this thread's first one on
+  auto phase_a = [&](unsigned k) {
+    const int slot = k % SCAN_SLOTS, buf = k & 1;
+    const IO* const dt = s.dt + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
+    const IO* const x = s.x + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
+    float de[SCAN_R];
 #pragma unroll
-    for (int i = 0; i < SCAN_R / 2; ++i) {
-      const int t = warp * SCAN_R + 2 * i, at = (slot * SCAN_T + t) * 32 + lane;
-      const float v0 = to_f<IO>(s.dt[at]) + bias, v1 = to_f<IO>(s.dt[at + 32]) + bias;
-      float d0 = v0, d1 = v1;
-      if (p.softplus) unpair(softplus2(v0, v1), d0, d1);
-      if (tile * SCAN_T + t >= w.len) d0 = 0.f;
-      if (tile * SCAN_T + t + 1 >= w.len) d1 = 0.f;
-      if (MODE == SCAN_ENDS) sum += d0 + d1;
-      de[i] = pair(d0, d1);
-      dx[i] = mul2(de[i], pair(to_f<IO>(s.x[at]), to_f<IO>(s.x[at + 32])));
+    for (int i = 0; i < SCAN_R; ++i) de[i] = to_f<IO>(dt[i * 32]) + bias;
+    if (p.softplus) {
+#pragma unroll
+      for (int i = 0; i < SCAN_R; ++i) de[i] = softplus(de[i]);
     }
-    reinterpret_cast<ulonglong2*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_ulonglong2(de[0], de[1]);
-    reinterpret_cast<ulonglong2*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] = make_ulonglong2(dx[0], dx[1]);
-    transpose_tile<IO>(s.b + slot * SCAN_T * N, N, s.tb + buf * NP * SCAN_LD);
-    if (MODE == SCAN_Y) transpose_tile<IO>(s.c + slot * SCAN_T * N, N, s.tc + buf * NP * SCAN_LD);
+    const int left = mine - (int)k * SCAN_T;
+    if (left < SCAN_R) {
+#pragma unroll
+      for (int i = 0; i < SCAN_R; ++i) de[i] = i < left ? de[i] : 0.f;
+    }
+    if (MODE == SCAN_ENDS) sum += (de[0] + de[1]) + (de[2] + de[3]);
+    reinterpret_cast<float4*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(de[0], de[1], de[2], de[3]);
+    reinterpret_cast<float4*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] =
+        make_float4(de[0] * to_f<IO>(x[0]), de[1] * to_f<IO>(x[32]), de[2] * to_f<IO>(x[64]), de[3] * to_f<IO>(x[96]));
+    transpose_tiles<IO, MODE == SCAN_Y>(s.b + slot * SCAN_T * N, s.c + slot * SCAN_T * N, N, s.tb + buf * (NP * SCAN_LD),
+                                        s.tc + buf * (NP * SCAN_LD));
   };
   f32x2 a2[J];  // a log2(e), twice
   float h[J];
   const f32x2 bias2 = twice(EXP_BIAS);
-  auto phase_b = [&](int tile) {
-    const int buf = tile & 1;
+  auto phase_b = [&](unsigned k) {
+    const int buf = k & 1;
     if (MODE == SCAN_CKPT && w.on) {
-      float* k = p.ckpt + (((long long)w.b * p.tiles + tile) * N + n0) * p.C + w.c;
+      float* to = p.ckpt + (((long long)w.b * p.tiles + w.tile0 + k) * N + n0) * p.C + w.c;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (n0 + j < N) k[(long long)j * p.C] = h[j];
+        if (n0 + j < N) to[(long long)j * p.C] = h[j];
     }
     const ulonglong2* de = reinterpret_cast<const ulonglong2*>(s.de) + buf * SCAN_W * 32 + lane;
     const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + buf * SCAN_W * 32 + lane;
@@ -312,32 +325,35 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 6 : (J <= 8 ? 4 : 2)) sc
         reinterpret_cast<ulonglong2*>(s.y)[((buf * SCAN_W + warp) * SCAN_W + q) * 32 + lane] = make_ulonglong2(y01, y23);
     }
   };
-  auto phase_c = [&](int tile) {
-    const int slot = tile % SCAN_SLOTS, buf = tile & 1;
-    f32x2 u[SCAN_R / 2] = {};
+  IO* out = MODE == SCAN_Y ? p.y.at(w.b, first + warp * SCAN_R) + w.c : nullptr;
+  auto phase_c = [&](unsigned k) {  // in order
+    const int slot = k % SCAN_SLOTS, buf = k & 1;
+    const ulonglong2* part = reinterpret_cast<const ulonglong2*>(s.y) + (buf * SCAN_W * SCAN_W + warp) * 32 + lane;
+    f32x2 u01 = part[0].x, u23 = part[0].y;
 #pragma unroll
-    for (int k = 0; k < SCAN_W; ++k) {
-      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(s.y)[((buf * SCAN_W + k) * SCAN_W + warp) * 32 + lane];
-      u[0] = add2(u[0], v.x), u[1] = add2(u[1], v.y);
-    }
+    for (int i = 1; i < SCAN_W; ++i) u01 = add2(u01, part[i * SCAN_W * 32].x), u23 = add2(u23, part[i * SCAN_W * 32].y);
     float v[SCAN_R];
-    unpair(u[0], v[0], v[1]), unpair(u[1], v[2], v[3]);
-    IO* out = p.y.at(w.b, tile * SCAN_T + warp * SCAN_R) + w.c;
-    const int left = w.on ? w.len - (tile * SCAN_T + warp * SCAN_R) : 0, st = (int)p.y.st;
+    unpair(u01, v[0], v[1]), unpair(u23, v[2], v[3]);
+    const IO* const x = s.x + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
+    const IO* const z = s.z + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) {
-      const int at = (slot * SCAN_T + warp * SCAN_R + i) * 32 + lane;
-      v[i] = fmaf(dskip, to_f<IO>(s.x[at]), v[i]);
-      if (gated) {
-        const float z = to_f<IO>(s.z[at]);
-        v[i] *= z * sigmoid(z);
+    for (int i = 0; i < SCAN_R; ++i) v[i] = fmaf(dskip, to_f<IO>(x[i * 32]), v[i]);
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < SCAN_R; ++i) {
+        const float zv = to_f<IO>(z[i * 32]);
+        v[i] *= zv * sigmoid(zv);
       }
-      if (i < left) out[(long long)i * st] = from_f<IO>(v[i]);
     }
+    const int left = w.on ? mine - (int)k * SCAN_T : 0, st = (int)p.y.st;
+#pragma unroll
+    for (int i = 0; i < SCAN_R; ++i)
+      if (i < left) out[(long long)i * st] = from_f<IO>(v[i]);
+    out += (long long)SCAN_T * st;
   };
 
-  copy(w.tile0);
-  copy(w.tile0 + 1);
+  copy(0);
+  copy(1);
   for (int i = threadIdx.x; i < 2 * (NP - N) * SCAN_LD; i += SCAN_W * 32) {  // states that are not there
     const int k = i / ((NP - N) * SCAN_LD), r = i % ((NP - N) * SCAN_LD) + (k * NP + N) * SCAN_LD;
     s.tb[r] = s.tc[r] = 0.f;
@@ -350,20 +366,20 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 6 : (J <= 8 ? 4 : 2)) sc
   }
   copies_wait<0>();
   __syncthreads();
-  if (w.tile0 < w.tile1) {
-    phase_a(w.tile0);
+  if (count) {
+    phase_a(0);
     __syncthreads();
   }
-  for (int tile = w.tile0; tile < w.tile1; ++tile) {
-    copy(tile + 2);
-    if (MODE == SCAN_Y && tile > w.tile0) phase_c(tile - 1);
-    phase_b(tile);
-    if (tile + 1 < w.tile1) phase_a(tile + 1);
+  for (int k = 0; k < count; ++k) {
+    copy(k + 2);
+    if (MODE == SCAN_Y && k > 0) phase_c(k - 1);
+    phase_b(k);
+    if (k + 1 < count) phase_a(k + 1);
     copies_wait<0>();
     __syncthreads();
   }
   if constexpr (MODE == SCAN_Y) {
-    if (w.tile0 < w.tile1) phase_c(w.tile1 - 1);
+    if (count) phase_c(count - 1);
     if (!w.on) return;
     const int t1 = min((w.tile0 + p.chunk_tiles) * SCAN_T, p.T);
     for (int t = max(w.len, w.tile0 * SCAN_T) + warp; t < t1; t += SCAN_W) p.y.at(w.b, t)[w.c] = from_f<IO>(0.f);
