@@ -158,7 +158,7 @@ ScanWs scan_backward_ws(const wtconv_scan_desc* d) {
   ScanWs w;
   const size_t bc = (size_t)scan_blocks(d) * d->G * d->B * d->T * d->N, tiles = ceil_div(d->T, SCAN_T);
   w.ckpt = 0;
-  w.part_b = w.ckpt + tiles * d->B * d->N * d->C;
+  w.part_b = w.ckpt + tiles * (SCAN_T / SCAN_S) * d->B * d->N * d->C;
   w.part_c = w.part_b + bc;
   w.part_a = w.part_c + bc;
   w.part_d = w.part_a + (size_t)d->B * d->C * d->N;
@@ -235,23 +235,23 @@ size_t scan_chunk_floats(const wtconv_scan_desc* d) {
   return chunks == 1 ? 0 : (size_t)chunks * d->B * d->C * (d->N + 1);
 }
 
-// Calls f with the states of a warp: N over the warps, rounded up.
-template <typename F> wtconv_status with_states(int N, F f) {
-  if (N <= 1 * SCAN_W) return f(Int<1>());
-  if (N <= 2 * SCAN_W) return f(Int<2>());
-  if (N <= 4 * SCAN_W) return f(Int<4>());
-  if (N <= 8 * SCAN_W) return f(Int<8>());
+// Calls f with the warps of a block: SCAN_J states each.
+template <typename F> wtconv_status with_warps(int N, F f) {
+  if (N <= SCAN_J) return f(Int<1>());
+  if (N <= 2 * SCAN_J) return f(Int<2>());
+  if (N <= 4 * SCAN_J) return f(Int<4>());
+  if (N <= 8 * SCAN_J) return f(Int<8>());
   return f(Int<16>());
 }
+static_assert(WTCONV_SCAN_MAX_N == 16 * SCAN_J, "a block has at most 16 warps");
 
 template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>& p, cudaStream_t st) {
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
-  return with_states(p.N, [&](auto J) {
-    const ScanSmem<IO> s(nullptr, p.N, J.value * SCAN_W);
-    const size_t smem = s.end - (char*)nullptr;
-    TRY((allow_smem(scan_forward_kernel<IO, MODE, J.value>, smem)));
-    scan_forward_kernel<IO, MODE, J.value><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
+  return with_warps(p.N, [&](auto W) {
+    const size_t smem = ScanSmem<IO>(nullptr, p.N, W.value).end - (char*)nullptr;
+    TRY((allow_smem(scan_forward_kernel<IO, MODE, W.value>, smem)));
+    scan_forward_kernel<IO, MODE, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
   });
 }
@@ -293,11 +293,14 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
   p.part_bias = ws + w.part_bias;
   TRY((run_scan_forward<IO, SCAN_CKPT>(d, p, ws + w.end, st)));
   p.chunks = 1;
+  p.chunk_tiles = p.tiles;
   const long long blocks = (long long)p.B * p.blocks * p.G;
-  const size_t smem = sizeof(float) * (3 * SCAN_T * 32 + 3 * SCAN_W * SCAN_T * 32 + 2 * p.N * SCAN_LD + 3 * p.N * 32);
-  TRY(allow_smem(scan_backward_kernel<IO>, smem));
-  scan_backward_kernel<IO><<<(unsigned)blocks, SCAN_W * 32, smem, st>>>(p);
-  TRY(launched());
+  TRY(with_warps(p.N, [&](auto W) {
+    const size_t smem = ScanGradSmem<IO>(nullptr, p.N, W.value).end - (char*)nullptr;
+    TRY((allow_smem(scan_backward_kernel<IO, W.value>, smem)));
+    scan_backward_kernel<IO, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
+    return launched();
+  }));
   const long long bc = (long long)p.G * p.B * p.T * p.N;
   launch_sum(p.part_b, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(db), p.B, p.T, p.N}, st);
   launch_sum(p.part_c, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(dc), p.B, p.T, p.N}, st);

@@ -1,12 +1,13 @@
 // Selective state space scan: forward, gradients, one token.
 //
-// A block owns 32 channels (a lane each) of one batch row and SCAN_W warps
-// that share out the N states; tokens go by in tiles of SCAN_T.  Per tile:
+// A block owns 32 channels (a lane each) of one batch row; its W warps share
+// out the N states, SCAN_J each in registers.  Tokens go by in tiles of
+// SCAN_T.  Per tile:
 //   A  the warps share out the tokens and turn dt and x into delta and
 //      delta x in shared memory, once for all states; b and c go there too;
-//   B  each warp runs the recurrence of its J states, which live in registers,
-//      four tokens at a time: J independent chains of multiply-adds, and sums
-//      over the warp's states without an exchange between lanes;
+//   B  each warp runs the recurrence of its states, four tokens at a time:
+//      SCAN_J independent chains of multiply-adds, and sums over the warp's
+//      states without an exchange between lanes;
 //   C  the warps share out the tokens again, join the warps' sums and apply
 //      d x and the gate.
 // Tokens behind a row's length get delta = 0, x = 0: they leave h as it is.
@@ -21,12 +22,12 @@
 
 namespace wtseq {
 
-constexpr int SCAN_T = 16;        // tokens of a tile
-constexpr int SCAN_W = 4;         // warps of a block
-constexpr int SCAN_R = SCAN_T / SCAN_W;  // tokens of a warp in A and C: one float4
-constexpr int SCAN_LD = SCAN_T + 4;      // floats between states in the b, c tiles
-constexpr int SCAN_SLOTS = 4;            // tiles of inputs in shared memory
-static_assert(SCAN_R == 4, "a thread's tokens of a tile are one float4");
+constexpr int SCAN_T = 16;           // tokens of a tile
+constexpr int SCAN_J = 4;            // states of a warp
+constexpr int SCAN_S = 8;            // tokens between the states kept for the gradients
+constexpr int SCAN_LD = SCAN_T + 4;  // floats between states in the b, c tiles
+constexpr int SCAN_SLOTS = 4;        // tiles of inputs in shared memory, forward
+constexpr int SCAN_GSLOTS = 3;       // ... gradients
 
 template <typename IO> struct ScanArgs {
   Rows<IO> x, dt, z, b, c, y, dy, dx, ddt, dz;
@@ -37,7 +38,7 @@ template <typename IO> struct ScanArgs {
   const int* lengths;
   float* ends;               // [chunks][B][N][C] states after each chunk from a zero start
   float* sums;               // [chunks][B][C] sums of delta over each chunk
-  float* ckpt;               // [B][tiles][N][C] states before each tile
+  float* ckpt;               // [B][tiles * SCAN_T / SCAN_S][N][C] states before every SCAN_S tokens
   float *part_b, *part_c;    // [C blocks][B][T][N]
   float *part_a;             // [B][C][N]
   float *part_d, *part_bias; // [B][C]
@@ -56,8 +57,6 @@ template <typename IO> struct ScanArgs {
 // multiply-add that forms them.
 constexpr float EXP_BIAS = 1.8e-8f * 1.4426950408889634f;
 
-__device__ __forceinline__ float step_size(float v, int use_softplus) { return use_softplus ? softplus(v) : v; }
-
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {  // zeros where not valid
   const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
   const int n = valid ? 16 : 0;
@@ -74,16 +73,17 @@ template <int PENDING> __device__ __forceinline__ void copies_wait() {
 template <typename IO> struct RowCopy {  // [SCAN_T][32 channels]
   static constexpr int E = 16 / sizeof(IO), PER = 32 / E, ROWS = 32 / PER;  // elements, chunks a row, rows a pass
   const IO* p;
-  int left, st, at;  // tokens left from the lane's first one on (none for a lane outside the channels)
+  int left, st, at;  // tokens left from the lane's first one on (for a lane outside the channels never any)
+  __device__ __forceinline__ RowCopy() {}
   __device__ __forceinline__ RowCopy(const Rows<IO>& r, int b, int t0, int stop, long long col, long long width, bool wide) {
     const int lane = threadIdx.x & 31, t = wide ? lane / PER : 0, k = wide ? lane % PER * E : lane;
     const bool ok = col + k < width;
     p = r.at(b, t0 + t) + (ok ? col + k : 0);
-    left = ok ? stop - t0 - t : 0;
+    left = ok ? stop - t0 - t : -(1 << 30);
     st = (int)r.st;
     at = t * 32 + k;
   }
-  __device__ __forceinline__ void tile(bool wide, IO* s) {
+  __device__ __forceinline__ void tile(bool wide, int dir, IO* s) {  // then on to the next (1) or the one before (-1)
     if (wide) {
 #pragma unroll
       for (int k = 0; k < SCAN_T; k += ROWS) copy16(s + at + k * 32, p + (long long)k * st, k < left);
@@ -91,54 +91,96 @@ template <typename IO> struct RowCopy {  // [SCAN_T][32 channels]
 #pragma unroll 4
       for (int k = 0; k < SCAN_T; ++k) s[at + k * 32] = k < left ? p[(long long)k * st] : from_f<IO>(0.f);
     }
-    left -= SCAN_T;
-    p += (long long)SCAN_T * st;
+    left -= dir * SCAN_T;
+    p += (long long)(dir * SCAN_T) * st;
   }
 };
-template <typename IO> struct StateCopy {  // [SCAN_T][N states]
-  static constexpr int E = 16 / sizeof(IO);
-  const IO* p;
-  int left, st, per, t, step;  // tokens left; chunks a row; the lane's first token, tokens a pass (0: not a whole number)
-  __device__ __forceinline__ StateCopy(const Rows<IO>& r, int b, int t0, int stop, long long col, int N, bool wide) {
-    const int lane = threadIdx.x & 31, e = wide ? E : 1;
+// The tiles of b or c, [SCAN_T][N states]: the chunks of a row of N, and the
+// lane's first token and state; `step` tokens a pass (0: not a whole number).
+struct StateLanes {
+  int per, t, k, step;
+  __device__ __forceinline__ StateLanes(int N, int e) {
+    const int lane = threadIdx.x & 31;
     per = N / e;
     t = lane / per;
+    k = (lane - t * per) * e;
     step = 32 % per ? 0 : 32 / per;
-    p = r.at(b, t0) + col;
-    left = stop - t0;
-    st = (int)r.st;
   }
-  __device__ __forceinline__ void one(int t, int k, bool wide, int N, IO* s) const {
+};
+template <typename IO>
+__device__ __forceinline__ void copy_states(const StateLanes& l, const Rows<IO>& r, const IO* p, int left, bool wide, int N, IO* s) {
+  const int st = (int)r.st;
+  auto one = [&](int t, int k) {
     if (wide)
       copy16(s + t * N + k, p + (long long)t * st + k, t < left);
     else
       s[t * N + k] = t < left ? p[(long long)t * st + k] : from_f<IO>(0.f);
+  };
+  if (l.step) {
+    for (int u = l.t; u < SCAN_T; u += l.step) one(u, l.k);
+  } else {
+    const int e = wide ? 16 / sizeof(IO) : 1;
+    for (int i = threadIdx.x & 31; i < SCAN_T * l.per; i += 32) one(i / l.per, i % l.per * e);
   }
-  __device__ __forceinline__ void tile(bool wide, int N, IO* s) {
-    const int lane = threadIdx.x & 31, e = wide ? E : 1;
-    if (step) {
-      const int k = (lane - t * per) * e;
-      for (int u = t; u < SCAN_T; u += step) one(u, k, wide, N, s);
-    } else {
-      for (int i = lane; i < SCAN_T * per; i += 32) one(i / per, i % per * e, wide, N, s);
+}
+
+// The copies that a warp makes of a tile: the inputs r = 0 .. R-1 and then b
+// and c are dealt to the warps in turn.
+template <typename IO, int W, int R> struct TileCopies {
+  static constexpr int MINE = (R + W - 1) / W;
+  RowCopy<IO> rows[MINE];
+  int to[MINE];  // the input's place among the slots, which follow one another; -1: none
+  StateLanes lanes;
+  const IO *bc, *other;  // the warp's next tile of b or c (of b and of c, where a block is one warp)
+  int left;      // tokens from there on
+  __device__ __forceinline__ TileCopies(const ScanArgs<IO>& p, const Rows<IO> (&in)[R], int row, int t0, int stop, long long col,
+                                        int g)
+      : lanes(p.N, p.wide_bc ? 16 / sizeof(IO) : 1), left(stop - t0) {
+    const int warp = threadIdx.x >> 5;
+    bc = (W == 1 || warp == R % W ? p.b : p.c).at(row, t0) + (long long)g * p.N;
+    other = p.c.at(row, t0) + (long long)g * p.N;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      Rows<IO> r = in[0];
+      to[i] = -1;
+#pragma unroll
+      for (int k = i * W; k < R && k < (i + 1) * W; ++k)
+        if (k == i * W + warp) r = in[k], to[i] = k;
+      if (!r.p) to[i] = -1;
+      if (to[i] >= 0) rows[i] = RowCopy<IO>(r, row, t0, stop, col, p.C, p.wide_x);
     }
-    left -= SCAN_T;
-    p += (long long)SCAN_T * st;
+  }
+  __device__ __forceinline__ void tile(const ScanArgs<IO>& p, int slot, int slots, int dir, IO* x, IO* to_b, IO* to_c) {
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i)
+      if (to[i] >= 0) rows[i].tile(p.wide_x, dir, x + (to[i] * slots + slot) * (SCAN_T * 32));
+    if (W == 1) {  // both
+      copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.N, to_b + slot * SCAN_T * p.N);
+      if (to_c) copy_states<IO>(lanes, p.c, other, left, p.wide_bc, p.N, to_c + slot * SCAN_T * p.N);
+      other += (long long)(dir * SCAN_T) * (int)p.c.st;
+    } else if (warp == R % W) {
+      copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.N, to_b + slot * SCAN_T * p.N);
+    } else if (to_c && warp == (R + 1) % W) {
+      copy_states<IO>(lanes, p.c, bc, left, p.wide_bc, p.N, to_c + slot * SCAN_T * p.N);
+    }
+    bc += (long long)(dir * SCAN_T) * (int)(W == 1 || warp == R % W ? p.b : p.c).st;
+    left -= dir * SCAN_T;
   }
 };
 
 // b and c of a tile, [t][n], as fp32 [n][t]: a thread per token and two states.
-template <typename IO, bool BOTH>
+template <typename IO, int W, bool BOTH>
 __device__ __forceinline__ void transpose_tiles(const IO* b, const IO* c, int N, float* tb, float* tc) {
   const int t = threadIdx.x % SCAN_T;
   if (N & 1) {
-    for (int n = threadIdx.x / SCAN_T; n < N; n += SCAN_W * 32 / SCAN_T) {
+    for (int n = threadIdx.x / SCAN_T; n < N; n += W * 32 / SCAN_T) {
       tb[n * SCAN_LD + t] = to_f<IO>(b[t * N + n]);
       if (BOTH) tc[n * SCAN_LD + t] = to_f<IO>(c[t * N + n]);
     }
     return;
   }
-  for (int n = threadIdx.x / SCAN_T * 2; n < N; n += SCAN_W * 64 / SCAN_T) {
+  for (int n = threadIdx.x / SCAN_T * 2; n < N; n += W * 64 / SCAN_T) {
     const Pack<IO, 2> u = *reinterpret_cast<const Pack<IO, 2>*>(b + t * N + n);
     tb[n * SCAN_LD + t] = to_f<IO>(u.v[0]);
     tb[(n + 1) * SCAN_LD + t] = to_f<IO>(u.v[1]);
@@ -192,15 +234,68 @@ template <typename IO> __device__ __forceinline__ float scan_start(const ScanArg
   return h;
 }
 
-enum { SCAN_Y, SCAN_ENDS, SCAN_CKPT };  // y; the chunks' ends and sums; the states before each tile
+enum { SCAN_Y, SCAN_ENDS, SCAN_CKPT };  // y; the chunks' ends and sums; the states before every SCAN_S tokens
 
-// Bytes of shared memory, and where its parts lie.
+// A thread's tokens of a tile in A and C are R = SCAN_T / W neighbours, kept as
+// [t / 4][lane][t % 4]: four tokens of a lane are one 16-byte access.
+template <int R> __device__ __forceinline__ int token_slot(int t, int lane) { return ((t >> 2) * 32 + lane) * 4 + (t & 3); }
+template <int R> __device__ __forceinline__ void put_tokens(float* s, const float (&v)[R]) {
+  if constexpr (R >= 4) {
+#pragma unroll
+    for (int i = 0; i < R; i += 4) *reinterpret_cast<float4*>(s + i * 32) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else if constexpr (R == 2) {
+    *reinterpret_cast<float2*>(s) = make_float2(v[0], v[1]);
+  } else {
+    s[0] = v[0];
+  }
+}
+template <int R> __device__ __forceinline__ void get_tokens(const float* s, float (&v)[R]) {
+  if constexpr (R >= 4) {
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(s + i * 32);
+      v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+    }
+  } else if constexpr (R == 2) {
+    const float2 u = *reinterpret_cast<const float2*>(s);
+    v[0] = u.x, v[1] = u.y;
+  } else {
+    v[0] = s[0];
+  }
+}
+// ... summed over the warps' parts
+template <int W, int R> __device__ __forceinline__ void sum_tokens(const float* s, float (&v)[R]) {
+  if constexpr (R >= 4) {
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+      ulonglong2 u = *reinterpret_cast<const ulonglong2*>(s + i * 32);
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(s + w * SCAN_T * 32 + i * 32);
+        u.x = add2(u.x, x.x), u.y = add2(u.y, x.y);
+      }
+      unpair(u.x, v[i], v[i + 1]), unpair(u.y, v[i + 2], v[i + 3]);
+    }
+    return;
+  }
+  get_tokens<R>(s, v);
+#pragma unroll
+  for (int w = 1; w < W; ++w) {
+    float u[R];
+    get_tokens<R>(s + w * SCAN_T * 32, u);
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] += u[i];
+  }
+}
+
+// Where the parts of the shared memory lie, and (end - start) its size.
 template <typename IO> struct ScanSmem {
-  IO *x, *dt, *z, *b, *c;  // [slots][T][32 or N]
-  float *de, *dx;          // [2][W][32] float4: delta, delta x
-  float *y;                // [2][W][W][32] float4: sums over a warp's states
-  float *tb, *tc;          // [2][NP][LD], NP: N rounded up to the warps' states
-  __host__ __device__ ScanSmem(char* s, int N, int NP) {
+  float *de, *dx;          // [2][T/4][32] float4: delta, delta x
+  float *y;                // [2][W][T/4][32] float4: sums over a warp's states
+  float *tb, *tc;          // [2][NP][LD], NP: the warps' states
+  IO *x, *dt, *z, *b, *c;  // [slots][T][32 or N], x to z one behind the other
+  char* end;
+  __host__ __device__ ScanSmem(char* s, int N, int W) {
     auto take = [&](size_t n) {
       char* r = s;
       s += (n + 15) / 16 * 16;
@@ -209,9 +304,9 @@ template <typename IO> struct ScanSmem {
     const size_t row = SCAN_SLOTS * SCAN_T * 32 * sizeof(IO), bc = SCAN_SLOTS * SCAN_T * N * sizeof(IO);
     de = (float*)take(2 * SCAN_T * 32 * 4);
     dx = (float*)take(2 * SCAN_T * 32 * 4);
-    y = (float*)take(2 * SCAN_W * SCAN_T * 32 * 4);
-    tb = (float*)take(2 * NP * SCAN_LD * 4);
-    tc = (float*)take(2 * NP * SCAN_LD * 4);
+    y = (float*)take(2 * W * SCAN_T * 32 * 4);
+    tb = (float*)take(2 * W * SCAN_J * SCAN_LD * 4);
+    tc = (float*)take(2 * W * SCAN_J * SCAN_LD * 4);
     x = (IO*)take(row);
     dt = (IO*)take(row);
     z = (IO*)take(row);
@@ -219,90 +314,80 @@ template <typename IO> struct ScanSmem {
     c = (IO*)take(bc);
     end = s;
   }
-  char* end;
 };
 
 // Turn k of the loop copies tile k+2, does C of tile k-1, B of tile k and A of
 // tile k+1: none reads what another of the same turn writes, so one barrier a
 // turn is enough and the warps' phases overlap.
-template <typename IO, int MODE, int J>
-__global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) scan_forward_kernel(const ScanArgs<IO> p) {
+template <typename IO, int MODE, int W>
+__global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_kernel(const ScanArgs<IO> p) {
   extern __shared__ __align__(16) char scan_smem[];
-  constexpr int NP = J * SCAN_W;
+  constexpr int J = SCAN_J, NP = J * W, R = SCAN_T / W;
   const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
-  const ScanSmem<IO> s(scan_smem, N, NP);
+  const ScanSmem<IO> s(scan_smem, N, W);
   const ScanPlace w = scan_place(p);
   const bool gated = MODE == SCAN_Y && p.z.p;
   if (MODE == SCAN_ENDS && w.chunk == p.chunks - 1) {  // nothing comes after
-    for (int n = warp; w.on && n < N; n += SCAN_W)
+    for (int n = warp; w.on && n < N; n += W)
       p.ends[(((long long)w.chunk * p.B + w.b) * N + n) * p.C + w.c] = scan_first(p, w, n);
     return;
   }
   const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f;
   const float dskip = MODE == SCAN_Y && p.d ? __ldg(p.d + w.c) : 0.f;
-
-  // warp 0 copies x, 1 dt, 2 z, 3 b and c
-  static_assert(SCAN_W == 4, "a warp for each input");
   const int first = w.tile0 * SCAN_T, count = max(0, w.tile1 - w.tile0);
-  RowCopy<IO> rows(warp == 2 && gated ? p.z : (warp == 1 ? p.dt : p.x), w.b, first, w.len, w.col, p.C, p.wide_x);
-  StateCopy<IO> rows_b(p.b, w.b, first, w.len, (long long)w.g * N, N, p.wide_bc);
-  StateCopy<IO> rows_c(p.c, w.b, first, w.len, (long long)w.g * N, N, p.wide_bc);
-  IO* const raw = warp == 0 ? s.x : (warp == 1 ? s.dt : s.z);
-  // the phases count tiles from the block's first; copies go in order
+  const Rows<IO> none = {nullptr, 0, 0}, in[3] = {p.x, p.dt, gated ? p.z : none};
+  TileCopies<IO, W, 3> copies(p, in, w.b, first, w.len, w.col, w.g);
+  // the phases count tiles from the block's first; copies and C go in order
   auto copy = [&](int k) {
-    if (k < count) {
-      const int slot = k % SCAN_SLOTS;
-      if (warp < 2 || warp == 2 && gated) {
-        rows.tile(p.wide_x, raw + slot * (SCAN_T * 32));
-      } else if (warp == 3) {
-        rows_b.tile(p.wide_bc, N, s.b + slot * SCAN_T * N);
-        if (MODE == SCAN_Y) rows_c.tile(p.wide_bc, N, s.c + slot * SCAN_T * N);
-      }
-    }
+    if (k < count) copies.tile(p, k % SCAN_SLOTS, SCAN_SLOTS, 1, s.x, s.b, MODE == SCAN_Y ? s.c : nullptr);
     copies_commit();
   };
-  float sum = 0.f;  // of this thread's delta
-  const int mine = w.len - first - warp * SCAN_R;  // tokens from this thread's first one on
+  float sum = 0.f;                               // of this thread's delta
+  const int mine = w.len - first - warp * R;     // tokens from this thread's first one on
+  const int own = token_slot<R>(warp * R, lane);  // its place in a tile
   auto phase_a = [&](unsigned k) {
     const int slot = k % SCAN_SLOTS, buf = k & 1;
-    const IO* const dt = s.dt + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
-    const IO* const x = s.x + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
-    float de[SCAN_R];
+    const IO* const dt = s.dt + (slot * SCAN_T + warp * R) * 32 + lane;
+    const IO* const x = s.x + (slot * SCAN_T + warp * R) * 32 + lane;
+    float de[R], dx[R];
 #pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) de[i] = to_f<IO>(dt[i * 32]) + bias;
+    for (int i = 0; i < R; ++i) de[i] = to_f<IO>(dt[i * 32]) + bias;
     if (p.softplus) {
 #pragma unroll
-      for (int i = 0; i < SCAN_R; ++i) de[i] = softplus(de[i]);
+      for (int i = 0; i < R; ++i) de[i] = softplus(de[i]);
     }
     const int left = mine - (int)k * SCAN_T;
-    if (left < SCAN_R) {
+    if (left < R) {
 #pragma unroll
-      for (int i = 0; i < SCAN_R; ++i) de[i] = i < left ? de[i] : 0.f;
+      for (int i = 0; i < R; ++i) de[i] = i < left ? de[i] : 0.f;
     }
-    if (MODE == SCAN_ENDS) sum += (de[0] + de[1]) + (de[2] + de[3]);
-    reinterpret_cast<float4*>(s.de)[(buf * SCAN_W + warp) * 32 + lane] = make_float4(de[0], de[1], de[2], de[3]);
-    reinterpret_cast<float4*>(s.dx)[(buf * SCAN_W + warp) * 32 + lane] =
-        make_float4(de[0] * to_f<IO>(x[0]), de[1] * to_f<IO>(x[32]), de[2] * to_f<IO>(x[64]), de[3] * to_f<IO>(x[96]));
-    transpose_tiles<IO, MODE == SCAN_Y>(s.b + slot * SCAN_T * N, s.c + slot * SCAN_T * N, N, s.tb + buf * (NP * SCAN_LD),
-                                        s.tc + buf * (NP * SCAN_LD));
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (MODE == SCAN_ENDS) sum += de[i];
+      dx[i] = de[i] * to_f<IO>(x[i * 32]);
+    }
+    put_tokens<R>(s.de + buf * SCAN_T * 32 + own, de);
+    put_tokens<R>(s.dx + buf * SCAN_T * 32 + own, dx);
+    transpose_tiles<IO, W, MODE == SCAN_Y>(s.b + slot * SCAN_T * N, s.c + slot * SCAN_T * N, N, s.tb + buf * (NP * SCAN_LD),
+                                           s.tc + buf * (NP * SCAN_LD));
   };
   f32x2 a2[J];  // a log2(e), twice
   float h[J];
   const f32x2 bias2 = twice(EXP_BIAS);
   auto phase_b = [&](unsigned k) {
     const int buf = k & 1;
-    if (MODE == SCAN_CKPT && w.on) {
-      float* to = p.ckpt + (((long long)w.b * p.tiles + w.tile0 + k) * N + n0) * p.C + w.c;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (n0 + j < N) to[(long long)j * p.C] = h[j];
-    }
-    const ulonglong2* de = reinterpret_cast<const ulonglong2*>(s.de) + buf * SCAN_W * 32 + lane;
-    const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + buf * SCAN_W * 32 + lane;
+    const ulonglong2* de = reinterpret_cast<const ulonglong2*>(s.de) + buf * SCAN_T * 8 + lane;
+    const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + buf * SCAN_T * 8 + lane;
     const float* tb = s.tb + (buf * NP + n0) * SCAN_LD;
     const float* tc = s.tc + (buf * NP + n0) * SCAN_LD;
 #pragma unroll
     for (int q = 0; q < SCAN_T / 4; ++q) {
+      if (MODE == SCAN_CKPT && q % (SCAN_S / 4) == 0 && w.on) {
+        float* to = p.ckpt + ((((long long)w.b * p.tiles + w.tile0 + k) * SCAN_T + q * 4) / SCAN_S * N + n0) * p.C + w.c;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (n0 + j < N) to[(long long)j * p.C] = h[j];
+      }
       const ulonglong2 d = de[q * 32], u = dx[q * 32];
       f32x2 y01 = 0, y23 = 0;
 #pragma unroll
@@ -322,39 +407,35 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) sc
         }
       }
       if (MODE == SCAN_Y)
-        reinterpret_cast<ulonglong2*>(s.y)[((buf * SCAN_W + warp) * SCAN_W + q) * 32 + lane] = make_ulonglong2(y01, y23);
+        reinterpret_cast<ulonglong2*>(s.y)[((buf * W + warp) * (SCAN_T / 4) + q) * 32 + lane] = make_ulonglong2(y01, y23);
     }
   };
-  IO* out = MODE == SCAN_Y ? p.y.at(w.b, first + warp * SCAN_R) + w.c : nullptr;
-  auto phase_c = [&](unsigned k) {  // in order
+  IO* out = MODE == SCAN_Y ? p.y.at(w.b, first + warp * R) + w.c : nullptr;
+  auto phase_c = [&](unsigned k) {
     const int slot = k % SCAN_SLOTS, buf = k & 1;
-    const ulonglong2* part = reinterpret_cast<const ulonglong2*>(s.y) + (buf * SCAN_W * SCAN_W + warp) * 32 + lane;
-    f32x2 u01 = part[0].x, u23 = part[0].y;
+    float v[R];
+    sum_tokens<W, R>(s.y + buf * W * SCAN_T * 32 + own, v);
+    const IO* const x = s.x + (slot * SCAN_T + warp * R) * 32 + lane;
+    const IO* const z = s.z + (slot * SCAN_T + warp * R) * 32 + lane;
 #pragma unroll
-    for (int i = 1; i < SCAN_W; ++i) u01 = add2(u01, part[i * SCAN_W * 32].x), u23 = add2(u23, part[i * SCAN_W * 32].y);
-    float v[SCAN_R];
-    unpair(u01, v[0], v[1]), unpair(u23, v[2], v[3]);
-    const IO* const x = s.x + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
-    const IO* const z = s.z + (slot * SCAN_T + warp * SCAN_R) * 32 + lane;
-#pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) v[i] = fmaf(dskip, to_f<IO>(x[i * 32]), v[i]);
+    for (int i = 0; i < R; ++i) v[i] = fmaf(dskip, to_f<IO>(x[i * 32]), v[i]);
     if (gated) {
 #pragma unroll
-      for (int i = 0; i < SCAN_R; ++i) {
+      for (int i = 0; i < R; ++i) {
         const float zv = to_f<IO>(z[i * 32]);
         v[i] *= zv * sigmoid(zv);
       }
     }
     const int left = w.on ? mine - (int)k * SCAN_T : 0, st = (int)p.y.st;
 #pragma unroll
-    for (int i = 0; i < SCAN_R; ++i)
+    for (int i = 0; i < R; ++i)
       if (i < left) out[(long long)i * st] = from_f<IO>(v[i]);
     out += (long long)SCAN_T * st;
   };
 
   copy(0);
   copy(1);
-  for (int i = threadIdx.x; i < 2 * (NP - N) * SCAN_LD; i += SCAN_W * 32) {  // states that are not there
+  for (int i = threadIdx.x; i < 2 * (NP - N) * SCAN_LD; i += W * 32) {  // states that are not there
     const int k = i / ((NP - N) * SCAN_LD), r = i % ((NP - N) * SCAN_LD) + (k * NP + N) * SCAN_LD;
     s.tb[r] = s.tc[r] = 0.f;
   }
@@ -382,7 +463,7 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) sc
     if (count) phase_c(count - 1);
     if (!w.on) return;
     const int t1 = min((w.tile0 + p.chunk_tiles) * SCAN_T, p.T);
-    for (int t = max(w.len, w.tile0 * SCAN_T) + warp; t < t1; t += SCAN_W) p.y.at(w.b, t)[w.c] = from_f<IO>(0.f);
+    for (int t = max(w.len, first) + warp; t < t1; t += W) p.y.at(w.b, t)[w.c] = from_f<IO>(0.f);
     // the chunk with the row's last token, or the first of an empty row
     if (p.state_out && w.chunk == max(0, (w.len + SCAN_T - 1) / SCAN_T - 1) / p.chunk_tiles)
 #pragma unroll
@@ -396,7 +477,7 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) sc
     if (!w.on) return;
     if (warp == 0) {
 #pragma unroll
-      for (int k = 1; k < SCAN_W; ++k) sum += s.y[k * 32 + lane];
+      for (int k = 1; k < W; ++k) sum += s.y[k * 32 + lane];
       p.sums[r * p.C + w.c] = sum;
     }
 #pragma unroll
@@ -405,172 +486,307 @@ __global__ void __launch_bounds__(SCAN_W * 32, J <= 4 ? 5 : (J <= 8 ? 4 : 2)) sc
   }
 }
 
-// b or c of the tile's tokens as [n][t] floats, zero behind the length.
-template <typename IO>
-__device__ __forceinline__ void scan_load_bc(const Rows<IO>& r, int b, int g, int t0, int len, int N, float* s) {
-  for (int i = threadIdx.x; i < SCAN_T * N; i += SCAN_W * 32) {
-    const int t = i / N, n = i - t * N;
-    s[n * SCAN_LD + t] = t0 + t < len ? to_f<IO>(r.at(b, t0 + t)[(long long)g * N + n]) : 0.f;
-  }
-}
-
-// v[i] summed over the 32 lanes, for 32 values at once: lane l returns the
-// sum of v[l].  Each turn halves the values and the lanes that they lie on.
-__device__ __forceinline__ float transpose_sum(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
-}
-
-// Gradients, tiles last to first, from the states before each tile.  With
-// dp = dy silu(z), e_t = c_t dp_t + a_{t+1} e_{t+1} (the gradient of h_t) and
-// k_t = a_t h_{t-1} (what is kept of the state):
+// Gradients, tiles last to first, from the states before every SCAN_S tokens.
+// With dp = dy silu(z), e_t = c_t dp_t + a_{t+1} e_{t+1} (the gradient of h_t)
+// and k_t = a_t h_{t-1} (what is kept of the state):
 //   dc = sum_c dp h   db = sum_c e delta x   da = sum e k delta
 //   ddelta = sum_n e (a k + b x)   dx = d dp + delta sum_n e b
-template <typename IO> __global__ void __launch_bounds__(SCAN_W * 32) scan_backward_kernel(ScanArgs<IO> p) {
-  extern __shared__ float smem[];
-  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* sd = smem;                       // [T][32] delta
-  float* sx = sd + SCAN_T * 32;           // [T][32] delta x
-  float* sg = sx + SCAN_T * 32;           // [T][32] dp
-  float* sy = sg + SCAN_T * 32;           // [3][W][T][32]: y, sum e a k, sum e b
-  float* sb = sy + 3 * SCAN_W * SCAN_T * 32;
-  float* sc = sb + N * SCAN_LD;
-  float* sa = sc + N * SCAN_LD;           // [N][32] a log2(e)
-  float* se = sa + N * 32;                // [N][32] e from the tile behind, decayed
-  float* sda = se + N * 32;               // [N][32] da
-  const int per = p.C / p.G;
-  const int blk = blockIdx.x % (p.blocks * p.G), b = blockIdx.x / (p.blocks * p.G);
-  const int g = blk / p.blocks, off = (blk % p.blocks) * 32 + lane;
-  const bool on = off < per;
-  const int c = g * per + (on ? off : 0);
-  const int len = row_length(p.lengths, b, p.T);
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + c) : 0.f, dskip = p.d ? __ldg(p.d + c) : 0.f;
-  float acc_d = 0.f, acc_bias = 0.f;
-  for (int n = warp; n < N; n += SCAN_W) {
-    sa[n * 32 + lane] = __ldg(p.a + (long long)c * N + n) * LOG2E;
-    se[n * 32 + lane] = on && p.dstate_out ? p.dstate_out[((long long)b * p.C + c) * N + n] : 0.f;
-    sda[n * 32 + lane] = 0.f;
+// The sums over the channels are sums over lanes.  They take an exchange a
+// value, but no selecting, because register j of lane l holds the state
+// j ^ (l & 3): neighbours that exchange two registers each complete one of the
+// two states.  Only the quarter that remains after two such turns is summed by
+// halving the values and the lanes that they lie on.
+template <typename IO> struct ScanGradSmem {
+  float *de, *dx, *dp;          // [T/4][32] float4: delta, delta x, dp
+  float* y;                     // [3][W][T/4][32] float4: sums over a warp's states of c h, e a k, e b
+  float *tb, *tc;               // [NP][LD]
+  IO *x, *dt, *dy, *z, *b, *c;  // [slots][T][32 or N], x to z one behind the other
+  char* end;
+  __host__ __device__ ScanGradSmem(char* s, int N, int W) {
+    auto take = [&](size_t n) {
+      char* r = s;
+      s += (n + 15) / 16 * 16;
+      return r;
+    };
+    const size_t row = SCAN_GSLOTS * SCAN_T * 32 * sizeof(IO), bc = SCAN_GSLOTS * SCAN_T * N * sizeof(IO);
+    de = (float*)take(SCAN_T * 32 * 4);
+    dx = (float*)take(SCAN_T * 32 * 4);
+    dp = (float*)take(SCAN_T * 32 * 4);
+    y = (float*)take(3 * W * SCAN_T * 32 * 4);
+    tb = (float*)take(W * SCAN_J * SCAN_LD * 4);
+    tc = (float*)take(W * SCAN_J * SCAN_LD * 4);
+    x = (IO*)take(row);
+    dt = (IO*)take(row);
+    dy = (IO*)take(row);
+    z = (IO*)take(row);
+    b = (IO*)take(bc);
+    c = (IO*)take(bc);
+    end = s;
   }
+};
+
+// The sums over the four lanes l ^ 0..3 of what they hold of one state, for
+// the state of register 0: fed register by register.
+__device__ __forceinline__ void quad_sum(int j, const float (&x)[4], float (&lo)[4], float (&hi)[4]) {
+  float (&v)[4] = j < 2 ? lo : hi;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (j % 2 == 0)
+      v[i] = x[i];
+    else
+      v[i] += __shfl_xor_sync(0xffffffffu, x[i], 1);
+    if (j == 3) lo[i] += __shfl_xor_sync(0xffffffffu, hi[i], 2);
+  }
+}
+
+template <typename IO, int W>
+__global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_kernel(const ScanArgs<IO> p) {
+  extern __shared__ __align__(16) char scan_smem[];
+  constexpr int J = SCAN_J, NP = J * W, R = SCAN_T / W;
+  static_assert(J == 4 && SCAN_S == 8 && SCAN_T == 2 * SCAN_S, "the exchanges below are written for these");
+  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
+  const ScanGradSmem<IO> s(scan_smem, N, W);
+  const ScanPlace w = scan_place(p);
+  const bool gated = p.z.p;
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f, dskip = p.d ? __ldg(p.d + w.c) : 0.f;
+  const int count = max(0, w.tile1 - w.tile0), last = (w.tile0 + count - 1) * SCAN_T;
+  const Rows<IO> in[4] = {p.x, p.dt, p.dy, p.z};
+  TileCopies<IO, W, 4> copies(p, in, w.b, max(last, 0), w.len, w.col, w.g);
+  // turn k works on the tile from token last - k * SCAN_T on
+  auto copy = [&](int k) {
+    if (k < count) copies.tile(p, k % SCAN_GSLOTS, SCAN_GSLOTS, -1, s.x, s.b, s.c);
+    copies_commit();
+  };
+  const int own = token_slot<R>(warp * R, lane);
+  float acc_d = 0.f, acc_bias = 0.f;
+  auto phase_a = [&](int k) {
+    const int at = (k % SCAN_GSLOTS * SCAN_T + warp * R) * 32 + lane;
+    const int left = w.on ? w.len - (last - k * SCAN_T) - warp * R : 0;
+    float de[R], dx[R], dp[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      de[i] = to_f<IO>(s.dt[at + i * 32]) + bias;
+      dp[i] = to_f<IO>(s.dy[at + i * 32]);
+    }
+    if (p.softplus) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) de[i] = softplus(de[i]);
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float z = to_f<IO>(s.z[at + i * 32]);
+        dp[i] *= z * sigmoid(z);
+      }
+    }
+    if (left < R) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) de[i] = i < left ? de[i] : 0.f, dp[i] = i < left ? dp[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) dx[i] = i < left ? de[i] * to_f<IO>(s.x[at + i * 32]) : 0.f;
+    put_tokens<R>(s.de + own, de);
+    put_tokens<R>(s.dx + own, dx);
+    put_tokens<R>(s.dp + own, dp);
+    transpose_tiles<IO, W, true>(s.b + k % SCAN_GSLOTS * SCAN_T * N, s.c + k % SCAN_GSLOTS * SCAN_T * N, N, s.tb, s.tc);
+  };
+
+  // the states of this lane's registers
+  int nj[J];
+  f32x2 a2[J], da2[J];
+  float e[J], kept[J];  // kept: states before the next SCAN_S tokens to do
+  const f32x2 bias2 = twice(EXP_BIAS);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    nj[j] = n0 + (j ^ (lane & 3));
+    const bool there = nj[j] < N;
+    a2[j] = twice(there ? __ldg(p.a + (long long)w.c * N + nj[j]) * LOG2E : 0.f);
+    e[j] = there && w.on && p.dstate_out ? p.dstate_out[((long long)w.b * p.C + w.c) * N + nj[j]] : 0.f;
+    da2[j] = 0;
+  }
+  auto fetch = [&](int token) {
+    const long long r = ((long long)w.b * p.tiles * SCAN_T + token) / SCAN_S;
+#pragma unroll
+    for (int j = 0; j < J; ++j) kept[j] = token >= 0 && nj[j] < N ? __ldg(p.ckpt + (r * N + nj[j]) * p.C + w.c) : 0.f;
+  };
   // [C blocks of the group][B][T][N] partial sums over this block's channels
-  const long long part0 = (((long long)(blk % p.blocks) * p.G + g) * p.B + b) * p.T;
-  for (int tile = (len + SCAN_T - 1) / SCAN_T - 1; tile >= 0; --tile) {
-    const int t0 = tile * SCAN_T;
-    float xr[SCAN_R], zr[SCAN_R], vr[SCAN_R], gr[SCAN_R];
+  const int blk = blockIdx.x % (p.blocks * p.G) % p.blocks;
+  const long long part0 = (((long long)blk * p.G + w.g) * p.B + w.b) * p.T;
+  float* const part = (lane & 16 ? p.part_c : p.part_b) + part0 * N + n0 + (lane & 3);
+  auto phase_b = [&](int k) {
+    const int t0 = last - k * SCAN_T;
+#pragma unroll 1
+    for (int sub = SCAN_T / SCAN_S - 1; sub >= 0; --sub) {
+      const ulonglong2* de = reinterpret_cast<const ulonglong2*>(s.de) + sub * 64 + lane;
+      const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + sub * 64 + lane;
+      const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(s.dp) + sub * 64 + lane;
+      ulonglong2* sy = reinterpret_cast<ulonglong2*>(s.y) + (warp * 4 + sub * 2) * 32 + lane;
+      float h[J], v[16];  // v: db, then dc, of SCAN_S tokens
+      f32x2 kv[2][J][2];
 #pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) {
-      const int t = warp * SCAN_R + i;
-      float delta = 0.f, dp = 0.f;
-      xr[i] = zr[i] = vr[i] = gr[i] = 0.f;
-      if (on && t0 + t < len) {
-        xr[i] = to_f<IO>(p.x.at(b, t0 + t)[c]);
-        vr[i] = to_f<IO>(p.dt.at(b, t0 + t)[c]) + bias;
-        gr[i] = dp = to_f<IO>(p.dy.at(b, t0 + t)[c]);
-        if (p.z.p) {
-          zr[i] = to_f<IO>(p.z.at(b, t0 + t)[c]);
-          dp *= zr[i] * sigmoid(zr[i]);
+      for (int j = 0; j < J; ++j) h[j] = w.on ? kept[j] : 0.f;
+      fetch(t0 + (sub - 1) * SCAN_S);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const ulonglong2 d = de[q * 32], u = dx[q * 32], g = dp[q * 32];
+        f32x2 y01 = 0, y23 = 0;
+        float lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s.tb + nj[j] * SCAN_LD + sub * SCAN_S + 4 * q);
+          const ulonglong2 cq = *reinterpret_cast<const ulonglong2*>(s.tc + nj[j] * SCAN_LD + sub * SCAN_S + 4 * q);
+          float e0, e1, e2, e3, b0, b1, b2, b3;
+          unpair(fma2(d.x, a2[j], bias2), e0, e1), unpair(fma2(d.y, a2[j], bias2), e2, e3);
+          unpair(mul2(u.x, bq.x), b0, b1), unpair(mul2(u.y, bq.y), b2, b3);
+          e0 = exp2_approx(e0), e1 = exp2_approx(e1), e2 = exp2_approx(e2), e3 = exp2_approx(e3);
+          const float k0 = e0 * h[j], h0 = k0 + b0, k1 = e1 * h0, h1 = k1 + b1, k2 = e2 * h1, h2 = k2 + b2, k3 = e3 * h2;
+          h[j] = k3 + b3;
+          kv[q][j][0] = pair(k0, k1), kv[q][j][1] = pair(k2, k3);
+          const f32x2 h01 = pair(h0, h1), h23 = pair(h2, h[j]);
+          y01 = fma2(cq.x, h01, y01), y23 = fma2(cq.y, h23, y23);
+          float x[4];
+          unpair(mul2(g.x, h01), x[0], x[1]), unpair(mul2(g.y, h23), x[2], x[3]);
+          quad_sum(j, x, lo, hi);
         }
-        delta = step_size(vr[i], p.softplus);
+        sy[q * 32] = make_ulonglong2(y01, y23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[8 + q * 4 + i] = lo[i];
       }
-      sd[t * 32 + lane] = delta;
-      sx[t * 32 + lane] = delta * xr[i];
-      sg[t * 32 + lane] = dp;
+#pragma unroll
+      for (int q = 1; q >= 0; --q) {
+        const ulonglong2 d = de[q * 32], u = dx[q * 32], g = dp[q * 32];
+        float g0, g1, g2, g3;
+        unpair(g.x, g0, g1), unpair(g.y, g2, g3);
+        f32x2 ek01 = 0, ek23 = 0, eb01 = 0, eb23 = 0;
+        float lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s.tb + nj[j] * SCAN_LD + sub * SCAN_S + 4 * q);
+          const ulonglong2 cq = *reinterpret_cast<const ulonglong2*>(s.tc + nj[j] * SCAN_LD + sub * SCAN_S + 4 * q);
+          float c0, c1, c2, c3, a0, a1, a2_, a3;
+          unpair(cq.x, c0, c1), unpair(cq.y, c2, c3);
+          // the decays again: an exponential costs less than the registers that would keep it
+          unpair(fma2(d.x, a2[j], bias2), a0, a1), unpair(fma2(d.y, a2[j], bias2), a2_, a3);
+          const float e3 = fmaf(c3, g3, e[j]), e2 = fmaf(c2, g2, exp2_approx(a3) * e3), e1 = fmaf(c1, g1, exp2_approx(a2_) * e2),
+                      e0 = fmaf(c0, g0, exp2_approx(a1) * e1);
+          e[j] = exp2_approx(a0) * e0;
+          const f32x2 e01 = pair(e0, e1), e23 = pair(e2, e3);
+          float x[4];
+          unpair(mul2(u.x, e01), x[0], x[1]), unpair(mul2(u.y, e23), x[2], x[3]);
+          quad_sum(j, x, lo, hi);
+          const f32x2 q01 = mul2(e01, kv[q][j][0]), q23 = mul2(e23, kv[q][j][1]);
+          ek01 = fma2(a2[j], q01, ek01), ek23 = fma2(a2[j], q23, ek23);
+          da2[j] = fma2(d.x, q01, da2[j]), da2[j] = fma2(d.y, q23, da2[j]);
+          eb01 = fma2(bq.x, e01, eb01), eb23 = fma2(bq.y, e23, eb23);
+        }
+        sy[W * SCAN_T * 8 + q * 32] = make_ulonglong2(ek01, ek23);
+        sy[2 * W * SCAN_T * 8 + q * 32] = make_ulonglong2(eb01, eb23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[q * 4 + i] = lo[i];
+      }
+      // over the eight groups of four lanes: lane bits 4, 3, 2 become the bits of db or dc and of the token
+#pragma unroll
+      for (int o = 8; o >= 2; o >>= 1) {
+        const bool up = lane & (2 * o);
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * o);
+        }
+      }
+      const int t = t0 + sub * SCAN_S + (lane >> 1 & 6);  // lane bits 3, 2 are the token's bits 2, 1
+      if (n0 + (lane & 3) < N) {
+        if (t < w.len) part[(long long)t * N] = v[0];
+        if (t + 1 < w.len) part[(long long)(t + 1) * N] = v[1];
+      }
     }
-    scan_load_bc<IO>(p.b, b, g, t0, len, N, sb);
-    scan_load_bc<IO>(p.c, b, g, t0, len, N, sc);
+  };
+  auto phase_c = [&](int k) {
+    const int at = (k % SCAN_GSLOTS * SCAN_T + warp * R) * 32 + lane, t = last - k * SCAN_T + warp * R;
+    const int left = w.on ? w.len - t : 0;
+    float y[R], ek[R], eb[R], de[R], dp[R];
+    sum_tokens<W, R>(s.y + own, y);
+    sum_tokens<W, R>(s.y + W * SCAN_T * 32 + own, ek);
+    sum_tokens<W, R>(s.y + 2 * W * SCAN_T * 32 + own, eb);
+    get_tokens<R>(s.de + own, de);
+    get_tokens<R>(s.dp + own, dp);
+    float dv[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float x = to_f<IO>(s.x[at + i * 32]);
+      y[i] = fmaf(dskip, x, y[i]);
+      dv[i] = fmaf(x, eb[i], LN2 * ek[i]);
+      if (i < left) acc_d = fmaf(dp[i], x, acc_d);
+      eb[i] = fmaf(dskip, dp[i], de[i] * eb[i]);
+    }
+    if (p.softplus) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) dv[i] *= sigmoid(to_f<IO>(s.dt[at + i * 32]) + bias);
+    }
+    if (gated) {
+      IO* const out = p.dz.at(w.b, t) + w.c;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float z = to_f<IO>(s.z[at + i * 32]), g = to_f<IO>(s.dy[at + i * 32]);
+        if (i < left) out[(long long)i * (int)p.dz.st] = from_f<IO>(g * y[i] * dsilu(z, sigmoid(z)));
+      }
+    }
+    IO *const out_x = p.dx.at(w.b, t) + w.c, *const out_t = p.ddt.at(w.b, t) + w.c;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (i >= left) continue;
+      out_x[(long long)i * (int)p.dx.st] = from_f<IO>(eb[i]);
+      out_t[(long long)i * (int)p.ddt.st] = from_f<IO>(dv[i]);
+      acc_bias += dv[i];
+    }
+  };
+
+  copy(0);
+  copy(1);
+  for (int i = threadIdx.x; i < (NP - N) * SCAN_LD; i += W * 32) s.tb[N * SCAN_LD + i] = s.tc[N * SCAN_LD + i] = 0.f;
+  fetch(last + SCAN_T - SCAN_S);
+  copies_wait<0>();
+  __syncthreads();
+  if (count) {
+    phase_a(0);
     __syncthreads();
-    float y[SCAN_T] = {}, ek[SCAN_T] = {}, eb[SCAN_T] = {};
-    for (int n = warp; n < N; n += SCAN_W) {
-      const float a = sa[n * 32 + lane];
-      float h = on ? p.ckpt[(((long long)b * p.tiles + tile) * N + n) * p.C + c] : 0.f;
-      float av[SCAN_T], kv[SCAN_T], v[32];
-#pragma unroll
-      for (int t = 0; t < SCAN_T; ++t) {
-        av[t] = exp2_approx(sd[t * 32 + lane] * a);
-        kv[t] = av[t] * h;
-        h = fmaf(sx[t * 32 + lane], sb[n * SCAN_LD + t], kv[t]);
-        y[t] = fmaf(sc[n * SCAN_LD + t], h, y[t]);
-        v[16 + t] = sg[t * 32 + lane] * h;
-      }
-      float e = se[n * 32 + lane], da = 0.f;
-#pragma unroll
-      for (int t = SCAN_T - 1; t >= 0; --t) {
-        e = fmaf(sc[n * SCAN_LD + t], sg[t * 32 + lane], e);
-        v[t] = e * sx[t * 32 + lane];
-        const float q = e * kv[t];
-        ek[t] = fmaf(a, q, ek[t]);
-        da = fmaf(sd[t * 32 + lane], q, da);
-        eb[t] = fmaf(e, sb[n * SCAN_LD + t], eb[t]);
-        e *= av[t];
-      }
-      se[n * 32 + lane] = e;
-      sda[n * 32 + lane] += da;
-      const float sum = transpose_sum(v);
-      const int t = lane & 15;
-      if (t0 + t < len) (lane < 16 ? p.part_b : p.part_c)[(part0 + t0 + t) * N + n] = sum;
-    }
-#pragma unroll
-    for (int t = 0; t < SCAN_T; ++t) {
-      sy[(warp * SCAN_T + t) * 32 + lane] = y[t];
-      sy[((SCAN_W + warp) * SCAN_T + t) * 32 + lane] = ek[t];
-      sy[((2 * SCAN_W + warp) * SCAN_T + t) * 32 + lane] = eb[t];
-    }
+  }
+  for (int k = 0; k < count; ++k) {
+    copy(k + 2);
+    phase_b(k);
+    copies_wait<0>();
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < SCAN_R; ++i) {
-      const int t = warp * SCAN_R + i;
-      if (!on || t0 + t >= len) continue;
-      float yv = dskip * xr[i], ekv = 0.f, ebv = 0.f;
-#pragma unroll
-      for (int w = 0; w < SCAN_W; ++w) {
-        yv += sy[(w * SCAN_T + t) * 32 + lane];
-        ekv += sy[((SCAN_W + w) * SCAN_T + t) * 32 + lane];
-        ebv += sy[((2 * SCAN_W + w) * SCAN_T + t) * 32 + lane];
-      }
-      const float dp = sg[t * 32 + lane], delta = sd[t * 32 + lane];
-      if (p.z.p) {
-        const float s = sigmoid(zr[i]);
-        p.dz.at(b, t0 + t)[c] = from_f<IO>(gr[i] * yv * dsilu(zr[i], s));
-      }
-      p.dx.at(b, t0 + t)[c] = from_f<IO>(fmaf(dskip, dp, delta * ebv));
-      float dv = fmaf(xr[i], ebv, LN2 * ekv);
-      if (p.softplus) dv *= sigmoid(vr[i]);
-      p.ddt.at(b, t0 + t)[c] = from_f<IO>(dv);
-      acc_d = fmaf(dp, xr[i], acc_d);
-      acc_bias += dv;
-    }
+    phase_c(k);  // reads its own tokens of what A wrote, and A writes them again
+    if (k + 1 < count) phase_a(k + 1);
     __syncthreads();
   }
   // rows behind the length
-  for (int t = len + warp; t < p.T; t += SCAN_W) {
-    if (on) {
-      p.dx.at(b, t)[c] = from_f<IO>(0.f);
-      p.ddt.at(b, t)[c] = from_f<IO>(0.f);
-      if (p.z.p) p.dz.at(b, t)[c] = from_f<IO>(0.f);
+  const int t1 = min((w.tile0 + p.chunk_tiles) * SCAN_T, p.T);
+  for (int t = max(w.len, w.tile0 * SCAN_T) + warp; t < t1; t += W) {
+    if (w.on) {
+      p.dx.at(w.b, t)[w.c] = from_f<IO>(0.f);
+      p.ddt.at(w.b, t)[w.c] = from_f<IO>(0.f);
+      if (gated) p.dz.at(w.b, t)[w.c] = from_f<IO>(0.f);
     }
     for (int n = lane; n < N; n += 32) p.part_b[(part0 + t) * N + n] = p.part_c[(part0 + t) * N + n] = 0.f;
   }
-  for (int n = warp; n < N; n += SCAN_W) {
-    if (!on) continue;
-    p.part_a[((long long)b * p.C + c) * N + n] = sda[n * 32 + lane];
-    if (p.dstate) p.dstate[((long long)b * p.C + c) * N + n] = se[n * 32 + lane];
-  }
-  sy[warp * 32 + lane] = acc_d;
-  sy[(SCAN_W + warp) * 32 + lane] = acc_bias;
-  __syncthreads();
-  if (warp < 2 && on) {
-    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < SCAN_W; ++w) v += sy[(warp * SCAN_W + w) * 32 + lane];
-    (warp ? p.part_bias : p.part_d)[(long long)b * p.C + c] = v;
+  for (int j = 0; j < J; ++j) {
+    if (!w.on || nj[j] >= N) continue;
+    const long long i = ((long long)w.b * p.C + w.c) * N + nj[j];
+    float a, b;
+    unpair(da2[j], a, b);
+    p.part_a[i] = a + b;
+    if (p.dstate) p.dstate[i] = e[j];
+  }
+  s.y[warp * 32 + lane] = acc_d;
+  s.y[(W + warp) * 32 + lane] = acc_bias;
+  __syncthreads();
+  if (warp == 0 && w.on) {
+#pragma unroll
+    for (int k = 1; k < W; ++k) acc_d += s.y[k * 32 + lane], acc_bias += s.y[(W + k) * 32 + lane];
+    p.part_d[(long long)w.b * p.C + w.c] = acc_d;
+    p.part_bias[(long long)w.b * p.C + w.c] = acc_bias;
   }
 }
 
@@ -588,8 +804,8 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs<IO> p, const in
   if (live) {
     const int N = p.N, g = c / (p.C / p.G);
     x = to_f<IO>(p.x.at(b, 0)[c]);
-    const float delta =
-        step_size(to_f<IO>(p.dt.at(b, 0)[c]) + (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f), p.softplus);
+    float delta = to_f<IO>(p.dt.at(b, 0)[c]) + (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f);
+    if (p.softplus) delta = softplus(delta);
     const IO* bv = p.b.at(b, 0) + (long long)g * N;
     const IO* cv = p.c.at(b, 0) + (long long)g * N;
     float* h = p.state_out + ((long long)b * p.C + c) * N;
