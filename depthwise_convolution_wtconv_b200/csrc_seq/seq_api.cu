@@ -77,10 +77,20 @@ wtconv_status check_causal(const wtconv_causal_desc* d) {
   return d->k > WTCONV_CAUSAL_MAX_K ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
 }
 
-long long causal_groups(const wtconv_causal_desc* d) {
-  return d->B * ceil_div(d->T, CAUSAL_GSTRIP * CAUSAL_GY);
+// Tokens of a thread's strip: long ones repeat little at their ends, short ones
+// give the GPU more threads.  The longest of 16 .. most that leaves `fill`
+// threads, of four channels each, for every SM.
+int causal_strip(const wtconv_causal_desc* d, int most, int fill) {
+  int strip = most;
+  while (strip > 16 && (long long)d->B * ceil_div(d->T, strip) * ceil_div(d->C, 4) < (long long)SMS * fill) strip /= 2;
+  return strip;
 }
-size_t causal_ws(const wtconv_causal_desc* d) { return (size_t)causal_groups(d) * d->C * (d->k + 1) * sizeof(float); }
+int causal_forward_strip(const wtconv_causal_desc* d) { return causal_strip(d, 64, 768); }
+int causal_grad_strip(const wtconv_causal_desc* d) { return causal_strip(d, 128, 256); }
+long long causal_grad_strips(const wtconv_causal_desc* d) { return ceil_div(d->T, causal_grad_strip(d) * CAUSAL_GY); }
+size_t causal_ws(const wtconv_causal_desc* d) {
+  return (size_t)(d->B * causal_grad_strips(d)) * d->C * (d->k + 1) * sizeof(float);
+}
 
 template <typename IO> CausalArgs<IO> causal_args(const wtconv_causal_desc* d, const wtconv_rows* x, const float* w,
                                                   const float* bias) {
@@ -400,9 +410,11 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
     a.state = static_cast<const IO*>(state);
     a.state_out = static_cast<IO*>(state_out);
     a.lengths = lengths;
-    a.strips = (int)ceil_div(T, CAUSAL_STRIP);
-    constexpr int V = sizeof(IO) == 2 ? 8 : 4;  // 16 bytes a thread and token
-    const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(y, V, e, B, T) && wide(state, V, e) && wide(state_out, V, e);
+    a.strip = causal_forward_strip(desc);
+    a.strips = (int)ceil_div(T, a.strip);
+    constexpr int V = 4;  // more would fill the registers with taps and windows
+    const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(y, V, e, B, T) && wide(state, V, e) &&
+                     wide(state_out, V, e);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return vec ? causal_forward<IO, V>(a, desc->k, st) : causal_forward<IO, 1>(a, desc->k, st);
   });
@@ -437,10 +449,11 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
     a.dstate = static_cast<IO*>(dstate);
     a.lengths = lengths;
     a.part = static_cast<float*>(ws);
-    a.strips = (int)ceil_div(T, CAUSAL_GSTRIP * CAUSAL_GY);
-    constexpr int V = 4;  // taps, windows and sums of 4 channels fill the registers
-    const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(dy, V, e, B, T) && wide(dx, V, e, B, T) &&
-                     wide(state, V, e) && wide(dstate_out, V, e) && wide(dstate, V, e);
+    a.strip = causal_grad_strip(desc);
+    a.strips = (int)causal_grad_strips(desc);
+    constexpr int V = sizeof(IO) == 2 ? 4 : 2;  // taps, windows, sums and loads ahead fill the registers
+    const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(dy, V, e, B, T) &&
+                     wide(dx, V, e, B, T) && wide(state, V, e) && wide(dstate_out, V, e) && wide(dstate, V, e);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return vec ? causal_backward<IO, V>(a, desc->k, dw, dbias, st) : causal_backward<IO, 1>(a, desc->k, dw, dbias, st);
   });
@@ -465,7 +478,7 @@ wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_ro
     a.y = rows_of<IO>(y);
     a.state_out = static_cast<IO*>(state);
     constexpr int V = 4;
-    const bool vec = C % V == 0 && wide(x, V, e, B, 1) && wide(y, V, e, B, 1) && wide(state, V, e);
+    const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, 1) && wide(y, V, e, B, 1) && wide(state, V, e);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return vec ? causal_step<IO, V>(a, desc->k, active, st) : causal_step<IO, 1>(a, desc->k, active, st);
   });

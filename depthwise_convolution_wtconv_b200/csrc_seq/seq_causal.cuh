@@ -9,9 +9,12 @@
 
 namespace wtseq {
 
-constexpr int CAUSAL_STRIP = 32;   // tokens of a forward thread
-constexpr int CAUSAL_GSTRIP = 32;  // tokens of a gradient thread
-constexpr int CAUSAL_GY = 8;       // strips of a gradient block
+constexpr int CAUSAL_GY = 8;  // strips of a gradient block
+// Tokens that the loops take in one piece, and whose loads are in flight: a
+// multiple of the taps, so that the window of the last K inputs goes round in
+// its registers and nothing is moved.  Forward at least 8, which keeps enough
+// bytes in flight; the gradients load two inputs and have fewer registers left.
+__host__ __device__ constexpr int causal_unroll(int K, int least) { return (least + K - 1) / K * K; }
 
 template <typename IO> struct CausalArgs {
   Rows<IO> x, y, dy, dx;
@@ -22,7 +25,32 @@ template <typename IO> struct CausalArgs {
   IO* dstate;
   const int* lengths;
   float* part;  // [groups][C][K+1]
-  int B, T, C, silu, strips;
+  int B, T, C, silu;
+  int strip, strips;  // tokens of a thread; strips (gradients: blocks of strips) of a row
+};
+
+// The V channels of a thread, as fp32 pairs where V is even: every operation
+// below is on a pair (or, for V = 1, on one value and a zero beside it).
+template <int V> struct Vals {
+  static constexpr int P = (V + 1) / 2;
+  f32x2 p[P];
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = pair(f[2 * i], 2 * i + 1 < V ? f[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.f);
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float lo, hi;
+      unpair(p[i], lo, hi);
+      f[2 * i] = lo;
+      if (2 * i + 1 < V) f[2 * i + 1 < V ? 2 * i + 1 : 0] = hi;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = 0;
+  }
 };
 
 // Input at token t (t < 0: of the state before the pass).
@@ -39,13 +67,43 @@ __device__ __forceinline__ void causal_input(const CausalArgs<IO>& a, int b, lon
 }
 
 template <typename IO, int K, int V>
-__device__ __forceinline__ void causal_taps(const CausalArgs<IO>& a, int c, float (&w)[K][V], float (&bias)[V]) {
+__device__ __forceinline__ void causal_taps(const CausalArgs<IO>& a, int c, Vals<V> (&w)[K], Vals<V>& bias) {
+  float f[K][V], g[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+  for (int i = 0; i < V; ++i) g[i] = a.bias ? __ldg(a.bias + c + i) : 0.f;
+  bias.set(g);
+  const float* p = a.w + (long long)c * K;  // V * K values in a row, 16-byte aligned where V is a multiple of 4
+  if constexpr (V % 4 == 0) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][i] = __ldg(a.w + (long long)(c + i) * K + j);
+    for (int q = 0; q < V * K / 4; ++q) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p) + q);
+      const float e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[(q * 4 + i) % K][(q * 4 + i) / K] = e[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * K; ++i) f[i % K][i / K] = __ldg(p + i);
   }
+#pragma unroll
+  for (int j = 0; j < K; ++j) w[j].set(f[j]);
+}
+
+// sum_j w[j] win[(first + j) % K] + v, win a ring
+template <int K, int V>
+__device__ __forceinline__ Vals<V> causal_sum(const Vals<V> (&w)[K], const Vals<V> (&win)[K], int first, Vals<V> v) {
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int i = 0; i < Vals<V>::P; ++i) v.p[i] = fma2(w[j].p[i], win[(first + j) % K].p[i], v.p[i]);
+  return v;
+}
+// 1 / (1 + exp(-v)) of a pair
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+  float a, b;
+  unpair(mul2(v, twice(-LOG2E)), a, b);
+  unpair(add2(pair(exp2_approx(a), exp2_approx(b)), twice(1.f)), a, b);
+  return pair(rcp_approx(a), rcp_approx(b));
 }
 
 template <typename IO, int K, int V> __global__ void __launch_bounds__(128) causal_forward_kernel(CausalArgs<IO> a) {
@@ -55,14 +113,26 @@ template <typename IO, int K, int V> __global__ void __launch_bounds__(128) caus
   const long long r = id / groups;
   const int b = (int)(r / a.strips);
   if (b >= a.B) return;
-  const int t0 = (int)(r % a.strips) * CAUSAL_STRIP;
-  const int t1 = min(t0 + CAUSAL_STRIP, a.T), len = row_length(a.lengths, b, a.T);
-  float w[K][V], bias[V], win[K][V];
-  causal_taps<IO, K, V>(a, c, w, bias);
+  const int t0 = (int)(r % a.strips) * a.strip;
+  const int t1 = min(t0 + a.strip, a.T), len = row_length(a.lengths, b, a.T);
   const int stop = min(t1, len);
+  constexpr int U = causal_unroll(K, 8);
+  const IO* in = a.x.at(b, t0) + c;  // of the next load: U tokens ahead of the work
+  IO* out = a.y.at(b, t0) + c;
+  const int xs = (int)a.x.st, ys = (int)a.y.st;
+  Raw<IO, V> raw[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i, in += xs)
+    if (t0 + i < stop) raw[i].load(in);
+  Vals<V> w[K], bias, win[K];
+  causal_taps<IO, K, V>(a, c, w, bias);
   if (t0 < len) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) causal_input<IO, K, V>(a, b, (long long)t0 - (K - 1) + j, c, win[j]);
+    for (int j = 0; j < K - 1; ++j) {
+      float f[V];
+      causal_input<IO, K, V>(a, b, (long long)t0 - (K - 1) + j, c, f);
+      win[j].set(f);
+    }
   }
   // the state after the pass, by the threads of the first strip, which alone
   // read the one before it (the two may be the same memory)
@@ -73,22 +143,22 @@ template <typename IO, int K, int V> __global__ void __launch_bounds__(128) caus
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) store_pack<IO, V>(a.state_out + ((long long)b * (K - 1) + j) * a.C + c, s[j]);
   }
-#pragma unroll 4
-  for (int t = t0; t < stop; ++t) {
-    load_pack<IO, V>(a.x.at(b, t) + c, win[K - 1]);
-    float o[V];
+  for (int t = t0; t < stop; t += U) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float p = bias[i];
+    for (int i = 0; i < U; ++i, in += xs, out += ys) {
+      if (t + i >= stop) break;
+      float f[V];
+      raw[i].floats(f);
+      if (t + U + i < stop) raw[i].load(in);
+      win[(i + K - 1) % K].set(f);
+      Vals<V> p = causal_sum<K, V>(w, win, i % K, bias);
+      if (a.silu) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-      o[i] = a.silu ? p * sigmoid(p) : p;
+        for (int v = 0; v < Vals<V>::P; ++v) p.p[v] = mul2(p.p[v], sigmoid2(p.p[v]));
+      }
+      p.get(f);
+      store_pack<IO, V>(out, f);
     }
-    store_pack<IO, V>(a.y.at(b, t) + c, o);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
   }
   const float zero[V] = {};
   for (int t = max(t0, stop); t < t1; ++t) store_pack<IO, V>(a.y.at(b, t) + c, zero);
@@ -102,84 +172,126 @@ template <typename IO, int K, int V> __global__ void __launch_bounds__(128) caus
 // order and go to the workspace.
 template <typename IO, int K, int V> __global__ void __launch_bounds__(256) causal_backward_kernel(CausalArgs<IO> a) {
   __shared__ float sums[CAUSAL_GY][32 * V];
+  constexpr int P = Vals<V>::P;
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int cblocks = (a.C / V + 31) / 32;
   const int cb = blockIdx.x % cblocks;
   const long long r = blockIdx.x / cblocks;
   const int b = (int)(r / a.strips);
-  const long long t0 = (r % a.strips * CAUSAL_GY + y) * CAUSAL_GSTRIP;
+  const long long first = (r % a.strips * CAUSAL_GY + y) * a.strip;
   const int c = (cb * 32 + lane) * V;
   const int len = row_length(a.lengths, b, a.T);
-  float dw[K][V] = {}, db[V] = {};
-  if (c < a.C && t0 < a.T) {
-    const long long t1 = min(t0 + CAUSAL_GSTRIP, (long long)a.T);
-    float w[K][V], bias[V], win[K][V] = {}, g[K][V] = {};
+  Vals<V> dw[K], db;
+#pragma unroll
+  for (int j = 0; j < K; ++j) dw[j].zero();
+  db.zero();
+  if (c < a.C && first < a.T) {
+    const int t0 = (int)first, t1 = (int)min(first + a.strip, (long long)a.T), stop = min(t1, len);
+    constexpr int U = causal_unroll(K, 4);
+    const int xs = (int)a.x.st, gs = (int)a.dy.st, os = (int)a.dx.st;
+    const IO *in = a.x.at(b, t0) + c, *in_g = a.dy.at(b, t0) + c;  // of the next load
+    IO* out = a.dx.at(b, (long long)t0 - (K - 1)) + c;              // of the input that is complete
+    Raw<IO, V> rx[U], rg[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i, in += xs, in_g += gs)
+      if (t0 + i < stop) rx[i].load(in), rg[i].load(in_g);
+    Vals<V> w[K], bias, win[K], g[K];  // rings: token t0 + i is win[(i + K - 1) % K] and g[K - 1 - i % K]
     causal_taps<IO, K, V>(a, c, w, bias);
+#pragma unroll
+    for (int j = 0; j < K; ++j) g[j].zero(), win[j].zero();
     if (t0 < len) {
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) causal_input<IO, K, V>(a, b, t0 - (K - 1) + j, c, win[j]);
+      for (int j = 0; j < K - 1; ++j) {
+        float f[V];
+        causal_input<IO, K, V>(a, b, (long long)t0 - (K - 1) + j, c, f);
+        win[j].set(f);
+      }
     }
-#pragma unroll 2
-    for (long long t = t0; t < t1 + K - 1; ++t) {
-      if (t < len) {
-        float d[V];
-        load_pack<IO, V>(a.x.at(b, t) + c, win[K - 1]);
-        load_pack<IO, V>(a.dy.at(b, t) + c, d);
-        const bool mine = t < t1;
+    // g of token t0 + i from its x and dy
+    auto gate = [&](int i, const float (&x)[V], const float (&dy)[V]) {
+      win[(i + K - 1) % K].set(x);
+      Vals<V>& d = g[K - 1 - i % K];
+      d.set(dy);
+      if (a.silu) {
+        const Vals<V> p = causal_sum<K, V>(w, win, i % K, bias);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (a.silu) {
-            float p = bias[i];
-#pragma unroll
-            for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-            d[i] *= dsilu(p, sigmoid(p));
-          }
-          g[K - 1][i] = d[i];
-          if (mine) {
-            db[i] += d[i];
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][i] = fmaf(d[i], win[j][i], dw[j][i]);
-          }
+        for (int v = 0; v < P; ++v) {  // silu' = s + p s (1 - s)
+          const f32x2 s = sigmoid2(p.p[v]), ps = mul2(p.p[v], s);
+          d.p[v] = mul2(d.p[v], fma2(ps, fma2(s, twice(-1.f), twice(1.f)), s));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[K - 1][i] = 0.f;
       }
-      const long long s = t - (K - 1);  // the input whose gradient is complete
-      if (s >= t0 || (t0 == 0 && K > 1)) {
-        float o[V];
+    };
+    // the gradient of the input at t0 + i - (K - 1): sum_j w[j] g of token t0 + i - j
+    auto complete = [&](int i) {
+      Vals<V> v;
+      v.zero();
+      return causal_sum<K, V>(w, g, K - 1 - i % K, v);
+    };
+    const bool top = t0 == 0 && a.dstate;
+    for (int t = t0; t < stop; t += U) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float v = 0.f;
+      for (int i = 0; i < U; ++i, in += xs, in_g += gs, out += os) {
+        if (t + i >= stop) break;
+        float x[V], dy[V];
+        rx[i].floats(x), rg[i].floats(dy);
+        if (t + U + i < stop) rx[i].load(in), rg[i].load(in_g);
+        gate(i, x, dy);
 #pragma unroll
-          for (int j = 0; j < K; ++j) v = fmaf(w[j][i], g[K - 1 - j][i], v);
-          o[i] = v;
+        for (int v = 0; v < P; ++v) {
+          const f32x2 d = g[K - 1 - i % K].p[v];
+          db.p[v] = add2(db.p[v], d);
+#pragma unroll
+          for (int j = 0; j < K; ++j) dw[j].p[v] = fma2(d, win[(i + j) % K].p[v], dw[j].p[v]);
         }
-        if (a.dstate_out && t >= len && t < (long long)len + K - 1) {
+        float f[V];
+        complete(i).get(f);
+        if (t + i - t0 >= K - 1)
+          store_pack<IO, V>(out, f);
+        else if (top)
+          store_pack<IO, V>(a.dstate + ((long long)b * (K - 1) + t + i) * a.C + c, f);
+      }
+    }
+    // the tokens of the next strip that this one's inputs reach, and those behind the length
+    const long long t2 = (long long)t1 + K - 1;
+    const int from = max(t0, stop), phase = (from - t0) % K;
+    for (long long t = from - phase; t < t2; t += K) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        if (t + i < from || t + i >= t2) continue;
+        if (t + i < len) {
+          float x[V], dy[V];
+          load_pack<IO, V>(a.x.at(b, t + i) + c, x), load_pack<IO, V>(a.dy.at(b, t + i) + c, dy);
+          gate(i, x, dy);
+        } else {
+          g[K - 1 - i].zero();
+        }
+        const long long s = t + i - (K - 1);
+        if (s < t0 && !top) continue;
+        float f[V];
+        complete(i).get(f);
+        if (a.dstate_out && t + i >= len && t + i < (long long)len + K - 1) {
           float d[V];
-          load_pack<IO, V>(a.dstate_out + ((long long)b * (K - 1) + (t - len)) * a.C + c, d);
+          load_pack<IO, V>(a.dstate_out + ((long long)b * (K - 1) + (t + i - len)) * a.C + c, d);
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] += d[i];
+          for (int v = 0; v < V; ++v) f[v] += d[v];
         }
-        if (s >= 0)
-          store_pack<IO, V>(a.dx.at(b, s) + c, o);
-        else if (a.dstate)
-          store_pack<IO, V>(a.dstate + ((long long)b * (K - 1) + (s + K - 1)) * a.C + c, o);
+        if (s >= t0)
+          store_pack<IO, V>(a.dx.at(b, s) + c, f);
+        else
+          store_pack<IO, V>(a.dstate + ((long long)b * (K - 1) + (s + K - 1)) * a.C + c, f);
       }
-#pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          win[j][i] = win[j + 1][i];
-          g[j][i] = g[j + 1][i];
-        }
     }
   }
   // part[r][c][0..K-1] = dw, [K] = dbias
 #pragma unroll
   for (int q = 0; q <= K; ++q) {
+    float f[V];
+    if (q < K)
+      dw[q < K ? q : 0].get(f);
+    else
+      db.get(f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) sums[y][lane * V + i] = q < K ? dw[q][i] : db[i];
+    for (int i = 0; i < V; ++i) sums[y][lane * V + i] = f[i];
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * V; i += 256) {
       float v = sums[0][i];
@@ -215,7 +327,8 @@ __global__ void __launch_bounds__(128) causal_step_kernel(CausalArgs<IO> a, cons
   if (b >= a.B) return;
   float o[V] = {};
   if (!active || __ldg(active + b)) {
-    float w[K][V], bias[V], win[K][V];
+    Vals<V> w[K], bias, u[K];
+    float win[K][V];
     IO* s = a.state_out + (long long)b * (K - 1) * a.C + c;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) load_pack<IO, V>(s + (long long)j * a.C, win[j]);
@@ -224,12 +337,13 @@ __global__ void __launch_bounds__(128) causal_step_kernel(CausalArgs<IO> a, cons
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) store_pack<IO, V>(s + (long long)j * a.C, win[j + 1]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float p = bias[i];
+    for (int j = 0; j < K; ++j) u[j].set(win[j]);
+    Vals<V> p = causal_sum<K, V>(w, u, 0, bias);
+    if (a.silu) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-      o[i] = a.silu ? p * sigmoid(p) : p;
+      for (int i = 0; i < Vals<V>::P; ++i) p.p[i] = mul2(p.p[i], sigmoid2(p.p[i]));
     }
+    p.get(o);
   }
   store_pack<IO, V>(a.y.at(b, 0) + c, o);
 }

@@ -44,6 +44,28 @@ template <typename IO, int V> __device__ __forceinline__ void load_pack(const IO
     for (int i = 0; i < W; ++i) f[k + i] = to_f<IO>(r.v[i]);
   }
 }
+// V channels as they lie in memory, to be had in flight and converted later.
+// Read-only loads: for inputs, which no output may overlap, so that loads may
+// pass the stores of earlier tokens.
+template <typename IO, int V> struct Raw {
+  static constexpr int W = sizeof(IO) * V <= 16 ? V : 16 / sizeof(IO);
+  Pack<IO, W> r[V / W];
+  __device__ __forceinline__ void load(const IO* p) {
+#pragma unroll
+    for (int k = 0; k < V / W; ++k) {
+      if constexpr (sizeof(Pack<IO, W>) == 16)
+        *reinterpret_cast<uint4*>(&r[k]) = __ldg(reinterpret_cast<const uint4*>(p + k * W));
+      else if constexpr (sizeof(Pack<IO, W>) == 8)
+        *reinterpret_cast<uint2*>(&r[k]) = __ldg(reinterpret_cast<const uint2*>(p + k * W));
+      else
+        r[k].v[0] = __ldg(p + k * W);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&f)[V]) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = to_f<IO>(r[k / W].v[k % W]);
+  }
+};
 template <typename IO, int V> __device__ __forceinline__ void store_pack(IO* p, const float (&f)[V]) {
   constexpr int W = sizeof(IO) * V <= 16 ? V : 16 / sizeof(IO);
 #pragma unroll
