@@ -341,7 +341,15 @@ wtconv_status check_norm_inputs(const wtconv_norm_desc* d, const wtconv_rows* x,
   return check_ptr(lengths, 4, false);
 }
 
-int norm_grad_blocks(const wtconv_norm_desc* d) { return (int)std::min<long long>((long long)d->B * d->T, SMS * 4); }
+// Blocks for rows that `threads` threads hold: enough for the SMs' registers,
+// so that each goes through its share of the rows (of the gradients, whose
+// blocks leave a partial sum each, fewer).
+int norm_blocks(const wtconv_norm_desc* d, int threads, int per_sm) {
+  const long long most = (long long)SMS * std::max(1, std::min(16, per_sm / threads));
+  return (int)std::min<long long>((long long)d->B * d->T, most);
+}
+// The most blocks of the gradients, whatever the variant: of one warp.
+int norm_grad_blocks(const wtconv_norm_desc* d) { return norm_blocks(d, 32, NORM_GRAD_THREADS); }
 
 template <typename IO, typename RES>
 NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, const wtconv_rows* gate, const float* w,
@@ -361,13 +369,13 @@ NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, con
   return a;
 }
 
-// Threads and chunks of a row: few values a thread while a block of 256 holds
-// the row, more for longer rows.  f gets V, NV and the threads.
+// Threads and chunks of a row: 8 values a thread while 512 threads hold the
+// row, then 16 and 32.  f gets V, NV and the threads.
 template <int V, typename F> wtconv_status norm_shape(int C, F f) {
   const int chunks = (int)ceil_div(C, V);
   constexpr int N1 = 8 / V, N2 = 16 / V, N3 = 32 / V;
   auto threads = [&](int nv) { return (int)ceil_div(ceil_div(chunks, nv), 32) * 32; };
-  if (threads(N1) <= 256) return f(Int<V>(), Int<N1>(), threads(N1));
+  if (threads(N1) <= 512) return f(Int<V>(), Int<N1>(), threads(N1));
   if (threads(N2) <= 512) return f(Int<V>(), Int<N2>(), threads(N2));
   return f(Int<V>(), Int<N3>(), threads(N3));
 }
@@ -604,8 +612,12 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
                        wide(y, V, sizeof(IO), B, T) && wide(res, V, sizeof(RES), B, T) &&
                        wide(res_out, V, sizeof(RES), B, T);
       return norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
-        norm_forward_kernel<IO, RES, v.value, nv.value>
-            <<<(unsigned)(B * T), threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        const int blocks = norm_blocks(desc, threads, v.value * nv.value <= 8 ? NORM_THREADS : 512);
+        if (v.value * nv.value <= 8 && threads <= 256)
+          norm_forward_kernel<IO, RES, v.value, nv.value, 256><<<blocks, threads, 0, st>>>(a);
+        else
+          norm_forward_kernel<IO, RES, v.value, nv.value, 512><<<blocks, threads, 0, st>>>(a);
         return launched();
       });
     });
@@ -651,8 +663,9 @@ wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_ro
                        wide(dx, V, e, B, T) && wide(dgate, V, e, B, T) && wide(res, V, re, B, T) &&
                        wide(dres_out, V, re, B, T) && wide(dres, V, re, B, T);
       cudaStream_t st = static_cast<cudaStream_t>(stream);
-      const int blocks = norm_grad_blocks(desc);
+      int blocks = 0;
       TRY((norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
+        blocks = norm_blocks(desc, threads, NORM_GRAD_THREADS);
         norm_backward_kernel<IO, RES, v.value, nv.value><<<blocks, threads, 0, st>>>(a);
         return launched();
       })));

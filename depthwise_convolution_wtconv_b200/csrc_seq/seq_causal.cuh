@@ -29,30 +29,6 @@ template <typename IO> struct CausalArgs {
   int strip, strips;  // tokens of a thread; strips (gradients: blocks of strips) of a row
 };
 
-// The V channels of a thread, as fp32 pairs where V is even: every operation
-// below is on a pair (or, for V = 1, on one value and a zero beside it).
-template <int V> struct Vals {
-  static constexpr int P = (V + 1) / 2;
-  f32x2 p[P];
-  __device__ __forceinline__ void set(const float (&f)[V]) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = pair(f[2 * i], 2 * i + 1 < V ? f[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.f);
-  }
-  __device__ __forceinline__ void get(float (&f)[V]) const {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float lo, hi;
-      unpair(p[i], lo, hi);
-      f[2 * i] = lo;
-      if (2 * i + 1 < V) f[2 * i + 1 < V ? 2 * i + 1 : 0] = hi;
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = 0;
-  }
-};
-
 // Input at token t (t < 0: of the state before the pass).
 template <typename IO, int K, int V>
 __device__ __forceinline__ void causal_input(const CausalArgs<IO>& a, int b, long long t, int c, float (&f)[V]) {
@@ -98,14 +74,6 @@ __device__ __forceinline__ Vals<V> causal_sum(const Vals<V> (&w)[K], const Vals<
     for (int i = 0; i < Vals<V>::P; ++i) v.p[i] = fma2(w[j].p[i], win[(first + j) % K].p[i], v.p[i]);
   return v;
 }
-// 1 / (1 + exp(-v)) of a pair
-__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
-  float a, b;
-  unpair(mul2(v, twice(-LOG2E)), a, b);
-  unpair(add2(pair(exp2_approx(a), exp2_approx(b)), twice(1.f)), a, b);
-  return pair(rcp_approx(a), rcp_approx(b));
-}
-
 template <typename IO, int K, int V> __global__ void __launch_bounds__(128) causal_forward_kernel(CausalArgs<IO> a) {
   const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
   const int groups = a.C / V;
@@ -215,10 +183,7 @@ template <typename IO, int K, int V> __global__ void __launch_bounds__(256) caus
       if (a.silu) {
         const Vals<V> p = causal_sum<K, V>(w, win, i % K, bias);
 #pragma unroll
-        for (int v = 0; v < P; ++v) {  // silu' = s + p s (1 - s)
-          const f32x2 s = sigmoid2(p.p[v]), ps = mul2(p.p[v], s);
-          d.p[v] = mul2(d.p[v], fma2(ps, fma2(s, twice(-1.f), twice(1.f)), s));
-        }
+        for (int v = 0; v < P; ++v) d.p[v] = mul2(d.p[v], dsilu2(p.p[v], sigmoid2(p.p[v])));
       }
     };
     // the gradient of the input at t0 + i - (K - 1): sum_j w[j] g of token t0 + i - j

@@ -132,6 +132,43 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+// 1 / (1 + exp(-v)) of a pair
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+  float a, b;
+  unpair(mul2(v, twice(-LOG2E)), a, b);
+  unpair(add2(pair(exp2_approx(a), exp2_approx(b)), twice(1.f)), a, b);
+  return pair(rcp_approx(a), rcp_approx(b));
+}
+
+// d silu(v) / dv = s + v s (1 - s), s = sigmoid(v), of a pair
+__device__ __forceinline__ f32x2 dsilu2(f32x2 v, f32x2 s) {
+  return fma2(mul2(v, s), fma2(s, twice(-1.f), twice(1.f)), s);
+}
+
+// The V channels of a thread, as fp32 pairs where V is even: every operation
+// below is on a pair (or, for V = 1, on one value and a zero beside it).
+template <int V> struct Vals {
+  static constexpr int P = (V + 1) / 2;
+  f32x2 p[P];
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = pair(f[2 * i], 2 * i + 1 < V ? f[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.f);
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float lo, hi;
+      unpair(p[i], lo, hi);
+      f[2 * i] = lo;
+      if (2 * i + 1 < V) f[2 * i + 1 < V ? 2 * i + 1 : 0] = hi;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = 0;
+  }
+};
+
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1.
 // log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, is s times a polynomial in
 // s^2 (degree 4, interpolated at the Chebyshev nodes of [0, 1/9]: off by less

@@ -1,9 +1,11 @@
 // Norms before and after a block with its gate and residual scale.
 //
-// A block of threads holds one row at a time in registers: NV chunks of V
-// neighbouring channels a thread, each input read once and each output
-// written once.  The gradients keep the sums over the rows for their channels
-// in registers while the block goes through its rows.
+// A block of threads holds one row at a time in registers, NV chunks of V
+// neighbouring channels a thread: each input is read once and each output
+// written once.  A block goes through its rows with the parameters of its
+// channels, and for the gradients the sums over the rows, in registers; where
+// these fit (8 values a thread) the next row's inputs are on their way while a
+// row is worked on.
 #pragma once
 
 #include "seq_common.cuh"
@@ -20,111 +22,204 @@ template <typename IO, typename RES> struct NormArgs {
   float eps;
 };
 
-// Sum over the block, for all of its threads; `s` holds a float per warp and
-// is not used again before a barrier.
-__device__ __forceinline__ float block_sum(float v, float* s) {
+constexpr int NORM_WARPS = 16;  // of a block, at most
+constexpr int NORM_THREADS = 1024, NORM_GRAD_THREADS = 512;  // of an SM
+
+// Sums over the block of N values, for all of its threads.  `s`: N rows of
+// NORM_WARPS floats, zero where there is no warp, which the block does not
+// write again before two more barriers.
+template <int N> __device__ __forceinline__ void block_sum(float (&v)[N], float (*s)[NORM_WARPS]) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  if (warps == 1) return;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k][threadIdx.x >> 5] = v[k];
+  }
   __syncthreads();
-  float r = 0.f;
-  for (int w = 0; w < warps; ++w) r += s[w];
-  return r;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0.f;
+#pragma unroll
+  for (int w = 0; w < NORM_WARPS; w += 4) {
+    if (w >= warps) break;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float4 u = *reinterpret_cast<const float4*>(s[k] + w);
+      v[k] += (u.x + u.y) + (u.z + u.w);
+    }
+  }
 }
 
-// One row's u and v: u = x silu(gate), n1 = 1 / sqrt(mean(u^2) + eps) (1
-// without w), v = u n1 w.
-template <typename IO, typename RES, int V, int NV>
-__device__ __forceinline__ void norm_u(const NormArgs<IO, RES>& a, int b, int t, float (&u)[NV][V]) {
+// The rows that a block goes through: every gridDim.x-th.
+struct NormRows {
+  int left, b, t, db, dt, T;  // rows to go; the present one
+  __device__ __forceinline__ NormRows(int B, int T) : T(T) {
+    left = B * T - (int)blockIdx.x;
+    b = blockIdx.x / T, t = blockIdx.x - b * T;
+    db = gridDim.x / T, dt = gridDim.x - db * T;
+  }
+  __device__ __forceinline__ void next() {
+    left -= gridDim.x, b += db, t += dt;
+    if (t >= T) t -= T, ++b;
+  }
+};
+template <typename IO> __device__ __forceinline__ IO* row_at(const Rows<IO>& r, int b, int t) {
+  return r.p + b * r.sb + (long long)t * (int)r.st;
+}
+
+// The fp32 parameters of a thread's channels: kept in registers, or loaded
+// where they are used.
+template <int V, int NV, bool KEEP> struct Params {
+  const float* p;
+  Vals<V> kept[KEEP ? NV : 1];
+  __device__ __forceinline__ Vals<V> load(int c, float none) const {
+    float f[V];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c >= a.C) {
+    for (int k = 0; k < V; ++k) f[k] = p ? __ldg(p + c + k) : none;
+    Vals<V> v;
+    v.set(f);
+    return v;
+  }
+  __device__ __forceinline__ Params(const float* from, int C, float none) : p(from) {
+    if constexpr (KEEP) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) u[i][k] = 0.f;
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        if (c < C)
+          kept[i] = load(c, none);
+        else
+          kept[i].zero();
+      }
+    }
+  }
+  __device__ __forceinline__ Vals<V> get(int i, int c, float none) const {
+    if constexpr (KEEP)
+      return kept[i];
+    else
+      return load(c, none);
+  }
+};
+
+// One row of an input as it lies in memory.
+template <typename IO, int V, int NV> struct RowIn {
+  Raw<IO, V> r[NV];
+  __device__ __forceinline__ void load(const Rows<IO>& in, int b, int t, int C) {
+    if (!in.p) return;
+    const IO* p = row_at(in, b, t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < C) r[i].load(p + c);
+    }
+  }
+};
+
+// NT: the most threads of a block.  Rows of 8 values a thread run at 64
+// registers, which fills an SM with 1024 threads.
+template <typename IO, typename RES, int V, int NV, int NT>
+__global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_forward_kernel(NormArgs<IO, RES> a) {
+  constexpr bool AHEAD = V * NV <= 8;
+  __shared__ __align__(16) float sums[2][2][1][NORM_WARPS];
+  for (int i = threadIdx.x; i < 4 * NORM_WARPS; i += blockDim.x) sums[0][0][0][i] = 0.f;
+  __syncthreads();
+  const float per = 1.f / a.C;
+  const Params<V, NV, AHEAD> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
+  RowIn<IO, V, NV> x, gate;
+  RowIn<RES, V, NV> res;
+  NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
+  auto load = [&] {
+    const int b = then.b, t = then.t;
+    if (then.left <= 0 || t >= row_length(a.lengths, b, a.T)) return;
+    x.load(a.x, b, t, a.C);
+    gate.load(a.gate, b, t, a.C);
+    res.load(a.res, b, t, a.C);
+  };
+  if (AHEAD) load(), then.next();
+  int turn = 0;
+  for (; now.left > 0; now.next(), turn ^= 1) {
+    const int b = now.b, t = now.t;
+    const bool live = t < row_length(a.lengths, b, a.T);
+    if (!AHEAD) load(), then.next();
+    float u[NV][V], r[NV][V];
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+#pragma unroll
+        for (int k = 0; k < V; ++k) u[i][k] = r[i][k] = 0.f;
+        if (c >= a.C) continue;
+        x.r[i].floats(u[i]);
+        if (a.gate.p) {
+          float g[V];
+          gate.r[i].floats(g);
+#pragma unroll
+          for (int k = 0; k < V; ++k) u[i][k] *= g[k] * sigmoid(g[k]);
+        }
+        if (a.res.p) res.r[i].floats(r[i]);
+      }
+    }
+    if (AHEAD) load(), then.next();
+    if (!live) {
+      const float zero[V] = {};
+      for (int c = threadIdx.x * V; c < a.C; c += blockDim.x * V) {
+        if (a.y.p) store_pack<IO, V>(row_at(a.y, b, t) + c, zero);
+        if (a.res_out.p) store_pack<RES, V>(row_at(a.res_out, b, t) + c, zero);
+      }
       continue;
     }
-    load_pack<IO, V>(a.x.at(b, t) + c, u[i]);
-    if (a.gate.p) {
-      float g[V];
-      load_pack<IO, V>(a.gate.at(b, t) + c, g);
+    if (a.w) {
+      float q[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < V; ++k) u[i][k] *= g[k] * sigmoid(g[k]);
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) q[0] = fmaf(u[i][k], u[i][k], q[0]);
+      block_sum(q, sums[turn][0]);
+      const float n1 = rsqrtf(fmaf(q[0], per, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        if (c >= a.C) continue;
+        float f[V];
+        w.get(i, c, 1.f).get(f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) u[i][k] *= n1 * f[k];
+      }
     }
-  }
-}
-
-template <int V, int NV> __device__ __forceinline__ float squares(const float (&u)[NV][V]) {
-  float s = 0.f;
+    float n2 = 1.f;
+    if (a.res.p) {
+      float q[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * V;
+        if (c >= a.C) continue;
+        float f[V];
+        scale.get(i, c, 1.f).get(f);
 #pragma unroll
-    for (int k = 0; k < V; ++k) s = fmaf(u[i][k], u[i][k], s);
-  return s;
-}
-
-template <int V> __device__ __forceinline__ void load_param(const float* p, int c, float (&f)[V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) f[k] = __ldg(p + c + k);
-}
-
-template <typename IO, typename RES, int V, int NV>
-__global__ void __launch_bounds__(V * NV <= 8 ? 256 : 512) norm_forward_kernel(NormArgs<IO, RES> a) {
-  __shared__ float s1[32], s2[32];
-  const int b = (int)(blockIdx.x / a.T), t = (int)(blockIdx.x % a.T);
-  const float zero[V] = {};
-  if (t >= row_length(a.lengths, b, a.T)) {
-    for (int c = threadIdx.x * V; c < a.C; c += blockDim.x * V) {
-      if (a.y.p) store_pack<IO, V>(a.y.at(b, t) + c, zero);
-      if (a.res_out.p) store_pack<RES, V>(a.res_out.at(b, t) + c, zero);
+        for (int k = 0; k < V; ++k) {
+          u[i][k] = fmaf(f[k], u[i][k], r[i][k]);
+          q[0] = fmaf(u[i][k], u[i][k], q[0]);
+        }
+        store_pack<RES, V>(row_at(a.res_out, b, t) + c, u[i]);
+      }
+      if (!a.w_res) continue;
+      block_sum(q, sums[turn][1]);
+      n2 = rsqrtf(fmaf(q[0], per, a.eps));
     }
-    return;
-  }
-  float u[NV][V];
-  norm_u<IO, RES, V, NV>(a, b, t, u);
-  if (a.w) {
-    const float n1 = rsqrtf(block_sum(squares<V, NV>(u), s1) / a.C + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
       if (c >= a.C) continue;
-      float w[V];
-      load_param<V>(a.w, c, w);
+      float f[V];
+      if (a.w_res) {
+        w_res.get(i, c, 1.f).get(f);
 #pragma unroll
-      for (int k = 0; k < V; ++k) u[i][k] *= n1 * w[k];
+        for (int k = 0; k < V; ++k) u[i][k] *= n2 * f[k];
+      }
+      store_pack<IO, V>(row_at(a.y, b, t) + c, u[i]);
     }
-  }
-  float n2 = 1.f;
-  if (a.res.p) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c >= a.C) continue;
-      float r[V], sc[V];
-      load_pack<RES, V>(a.res.at(b, t) + c, r);
-#pragma unroll
-      for (int k = 0; k < V; ++k) sc[k] = 1.f;
-      if (a.scale) load_param<V>(a.scale, c, sc);
-#pragma unroll
-      for (int k = 0; k < V; ++k) u[i][k] = fmaf(sc[k], u[i][k], r[k]);
-      store_pack<RES, V>(a.res_out.at(b, t) + c, u[i]);
-    }
-    if (!a.w_res) return;
-    n2 = rsqrtf(block_sum(squares<V, NV>(u), s2) / a.C + a.eps);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c >= a.C) continue;
-    if (a.w_res) {
-      float w[V];
-      load_param<V>(a.w_res, c, w);
-#pragma unroll
-      for (int k = 0; k < V; ++k) u[i][k] *= n2 * w[k];
-    }
-    store_pack<IO, V>(a.y.at(b, t) + c, u[i]);
   }
 }
 
@@ -134,141 +229,182 @@ __global__ void __launch_bounds__(V * NV <= 8 ? 256 : 512) norm_forward_kernel(N
 //   dw = sum q u n1   du = n1 q w - u n1^3 mean(u q w)
 //   dx = du silu(gate)   dgate = du x silu'(gate)
 template <typename IO, typename RES, int V, int NV>
-__global__ void __launch_bounds__(V * NV <= 8 ? 256 : 512) norm_backward_kernel(NormArgs<IO, RES> a) {
-  __shared__ float s[4][32];
-  float aw[NV][V] = {}, as[NV][V] = {}, ar[NV][V] = {};
-  const long long rows = (long long)a.B * a.T;
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int b = (int)(row / a.T), t = (int)(row % a.T);
-    if (t >= row_length(a.lengths, b, a.T)) {
+__global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES> a) {
+  constexpr bool AHEAD = V * NV <= 8;
+  constexpr int P = Vals<V>::P;
+  __shared__ __align__(16) float s1[2][1][NORM_WARPS], s2[2][2][NORM_WARPS], s3[2][1][NORM_WARPS];
+  for (int i = threadIdx.x; i < 2 * NORM_WARPS; i += blockDim.x) s1[0][0][i] = s2[0][0][i] = s2[1][0][i] = s3[0][0][i] = 0.f;
+  __syncthreads();
+  const float per = 1.f / a.C;
+  const Params<V, NV, AHEAD> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
+  Vals<V> aw[NV], as[NV], ar[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) aw[i].zero(), as[i].zero(), ar[i].zero();
+  RowIn<IO, V, NV> x, gate, dy;
+  RowIn<RES, V, NV> res, dres;
+  NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
+  auto load = [&] {
+    const int b = then.b, t = then.t;
+    if (then.left <= 0 || t >= row_length(a.lengths, b, a.T)) return;
+    x.load(a.x, b, t, a.C);
+    gate.load(a.gate, b, t, a.C);
+    res.load(a.res, b, t, a.C);
+    dy.load(a.dy, b, t, a.C);
+    dres.load(a.dres_out, b, t, a.C);
+  };
+  auto vals = [](const auto& raw) {
+    float f[V];
+    raw.floats(f);
+    Vals<V> v;
+    v.set(f);
+    return v;
+  };
+  auto total = [](f32x2 v) {
+    float lo, hi;
+    unpair(v, lo, hi);
+    return lo + hi;
+  };
+  if (AHEAD) load(), then.next();
+  int turn = 0;
+  for (; now.left > 0; now.next(), turn ^= 1) {
+    const int b = now.b, t = now.t;
+    const bool live = t < row_length(a.lengths, b, a.T);
+    if (!AHEAD) load(), then.next();
+    // u = x act; act = silu(gate) and xd = x silu'(gate) wait for the end
+    Vals<V> u[NV], act[NV], xd[NV], r[NV], q[NV], g[NV];
+    f32x2 uu = 0;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        u[i].zero(), act[i].zero(), xd[i].zero(), r[i].zero(), q[i].zero(), g[i].zero();
+        if ((i * blockDim.x + threadIdx.x) * V >= a.C) continue;
+        u[i] = vals(x.r[i]);
+        if (a.gate.p) {
+          act[i] = vals(gate.r[i]);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const f32x2 sg = sigmoid2(act[i].p[k]);
+            xd[i].p[k] = mul2(u[i].p[k], dsilu2(act[i].p[k], sg));
+            act[i].p[k] = mul2(act[i].p[k], sg);
+            u[i].p[k] = mul2(u[i].p[k], act[i].p[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) uu = fma2(u[i].p[k], u[i].p[k], uu);
+        if (a.res.p) r[i] = vals(res.r[i]);
+        if (a.dy.p) q[i] = vals(dy.r[i]);
+        if (a.dres_out.p) g[i] = vals(dres.r[i]);
+      }
+    }
+    if (AHEAD) load(), then.next();
+    if (!live) {
       const float zero[V] = {};
       for (int c = threadIdx.x * V; c < a.C; c += blockDim.x * V) {
-        store_pack<IO, V>(a.dx.at(b, t) + c, zero);
-        if (a.gate.p) store_pack<IO, V>(a.dgate.at(b, t) + c, zero);
-        if (a.res.p) store_pack<RES, V>(a.dres.at(b, t) + c, zero);
+        store_pack<IO, V>(row_at(a.dx, b, t) + c, zero);
+        if (a.gate.p) store_pack<IO, V>(row_at(a.dgate, b, t) + c, zero);
+        if (a.res.p) store_pack<RES, V>(row_at(a.dres, b, t) + c, zero);
       }
       continue;
     }
-    float u[NV][V], q[NV][V], n1 = 1.f;
-    norm_u<IO, RES, V, NV>(a, b, t, u);
-    if (a.w) n1 = rsqrtf(block_sum(squares<V, NV>(u), s[0]) / a.C + a.eps);
+    float n1 = 1.f;
+    if (a.w) {
+      float s[1] = {total(uu)};
+      block_sum(s, s1[turn]);
+      n1 = rsqrtf(fmaf(s[0], per, a.eps));
+    }
+    // from here on u is u n1
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < P; ++k) u[i].p[k] = mul2(u[i].p[k], twice(n1));
     if (a.res.p) {
-      float r[NV][V], n2 = 1.f, m = 0.f;
+      f32x2 rr = 0, rt = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) {
+        if (c >= a.C) continue;
+        const Vals<V> fs = scale.get(i, c, 1.f), fw = w.get(i, c, 1.f), fr = w_res.get(i, c, 1.f);
 #pragma unroll
-          for (int k = 0; k < V; ++k) r[i][k] = 0.f;
-          continue;
+        for (int k = 0; k < P; ++k) {
+          r[i].p[k] = fma2(fs.p[k], mul2(u[i].p[k], fw.p[k]), r[i].p[k]);
+          rr = fma2(r[i].p[k], r[i].p[k], rr);
+          rt = fma2(r[i].p[k], mul2(q[i].p[k], fr.p[k]), rt);
         }
-        float sc[V], w[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) sc[k] = w[k] = 1.f;
-        load_pack<RES, V>(a.res.at(b, t) + c, r[i]);
-        if (a.scale) load_param<V>(a.scale, c, sc);
-        if (a.w) load_param<V>(a.w, c, w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) r[i][k] = fmaf(sc[k], u[i][k] * n1 * w[k], r[i][k]);
       }
+      float n2 = 0.f, m = 0.f;
       if (a.w_res) {
-        n2 = rsqrtf(block_sum(squares<V, NV>(r), s[1]) / a.C + a.eps);
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (i * blockDim.x + threadIdx.x) * V;
-          if (c >= a.C) continue;
-          float w[V];
-          load_pack<IO, V>(a.dy.at(b, t) + c, q[i]);
-          load_param<V>(a.w_res, c, w);
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            ar[i][k] = fmaf(q[i][k], r[i][k] * n2, ar[i][k]);
-            q[i][k] *= w[k];
-            d = fmaf(r[i][k], q[i][k], d);
-          }
-        }
-        m = block_sum(d, s[2]) / a.C * n2 * n2 * n2;
+        float s[2] = {total(rr), total(rt)};
+        block_sum(s, s2[turn]);
+        n2 = rsqrtf(fmaf(s[0], per, a.eps));
+        m = -s[1] * per * n2 * n2 * n2;
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c >= a.C) continue;
-        float g[V] = {}, sc[V], w[V];
-        if (a.dres_out.p) load_pack<RES, V>(a.dres_out.at(b, t) + c, g);
+        const Vals<V> fs = scale.get(i, c, 1.f), fw = w.get(i, c, 1.f), fr = w_res.get(i, c, 1.f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          sc[k] = w[k] = 1.f;
-          if (a.w_res) g[k] += n2 * q[i][k] - r[i][k] * m;
+        for (int k = 0; k < P; ++k) {
+          const f32x2 qn = mul2(q[i].p[k], twice(n2));
+          ar[i].p[k] = fma2(qn, r[i].p[k], ar[i].p[k]);
+          g[i].p[k] = fma2(r[i].p[k], twice(m), fma2(qn, fr.p[k], g[i].p[k]));  // as it was, without w_res
+          as[i].p[k] = fma2(g[i].p[k], mul2(u[i].p[k], fw.p[k]), as[i].p[k]);
+          q[i].p[k] = mul2(g[i].p[k], fs.p[k]);
         }
-        store_pack<RES, V>(a.dres.at(b, t) + c, g);
-        if (a.scale) load_param<V>(a.scale, c, sc);
-        if (a.w) load_param<V>(a.w, c, w);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          as[i][k] = fmaf(g[k], u[i][k] * n1 * w[k], as[i][k]);
-          q[i][k] = g[k] * sc[k];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < a.C) load_pack<IO, V>(a.dy.at(b, t) + c, q[i]);
+        float f[V];
+        g[i].get(f);
+        store_pack<RES, V>(row_at(a.dres, b, t) + c, f);
       }
     }
     if (a.w) {
-      float d = 0.f;
+      f32x2 uq = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c >= a.C) continue;
-        float w[V];
-        load_param<V>(a.w, c, w);
+        const Vals<V> fw = w.get(i, c, 1.f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          aw[i][k] = fmaf(q[i][k], u[i][k] * n1, aw[i][k]);
-          q[i][k] *= w[k];
-          d = fmaf(u[i][k], q[i][k], d);
+        for (int k = 0; k < P; ++k) {
+          aw[i].p[k] = fma2(q[i].p[k], u[i].p[k], aw[i].p[k]);
+          q[i].p[k] = mul2(q[i].p[k], fw.p[k]);
+          uq = fma2(u[i].p[k], q[i].p[k], uq);
         }
       }
-      const float m = block_sum(d, s[3]) / a.C * n1 * n1 * n1;
+      float s[1] = {total(uq)};
+      block_sum(s, s3[turn]);
+      const float m = -s[0] * per * n1;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) q[i][k] = n1 * q[i][k] - u[i][k] * m;
+        for (int k = 0; k < P; ++k) q[i].p[k] = fma2(u[i].p[k], twice(m), mul2(q[i].p[k], twice(n1)));
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
       if (c >= a.C) continue;
+      float f[V];
       if (a.gate.p) {
-        float x[V], g[V], dg[V];
-        load_pack<IO, V>(a.x.at(b, t) + c, x);
-        load_pack<IO, V>(a.gate.at(b, t) + c, g);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float sg = sigmoid(g[k]);
-          dg[k] = q[i][k] * x[k] * dsilu(g[k], sg);
-          q[i][k] *= g[k] * sg;
+        for (int k = 0; k < P; ++k) {
+          xd[i].p[k] = mul2(xd[i].p[k], q[i].p[k]);
+          q[i].p[k] = mul2(q[i].p[k], act[i].p[k]);
         }
-        store_pack<IO, V>(a.dgate.at(b, t) + c, dg);
+        xd[i].get(f);
+        store_pack<IO, V>(row_at(a.dgate, b, t) + c, f);
       }
-      store_pack<IO, V>(a.dx.at(b, t) + c, q[i]);
+      q[i].get(f);
+      store_pack<IO, V>(row_at(a.dx, b, t) + c, f);
     }
-    __syncthreads();  // the next row's sums reuse s
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * blockDim.x + threadIdx.x) * V;
     if (c >= a.C) continue;
     float* p = a.part + (long long)blockIdx.x * 3 * a.C + c;
+    float f0[V], f1[V], f2[V];
+    aw[i].get(f0), as[i].get(f1), ar[i].get(f2);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      p[k] = aw[i][k];
-      p[a.C + k] = as[i][k];
-      p[2 * a.C + k] = ar[i][k];
-    }
+    for (int k = 0; k < V; ++k) p[k] = f0[k], p[a.C + k] = f1[k], p[2 * a.C + k] = f2[k];
   }
 }
 
