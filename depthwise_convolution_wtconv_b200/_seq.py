@@ -10,8 +10,10 @@ be passed in; `stream` selects the stream (default: the current one of the
 inputs' device), on which outputs and workspace are then allocated too.
 """
 import ctypes
+import struct
 
 import torch
+from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
 
 from ._lib import BF16, F32, _check, load
 
@@ -41,6 +43,7 @@ class NormDesc(ctypes.Structure):
 
 
 _bound = None
+_call = {}  # entries that take descriptors and rows as packed bytes, which are quicker to make than structures
 
 
 def load_seq():
@@ -60,83 +63,79 @@ def load_seq():
         "wtconv_scan_step": [sd, rp, rp, vp, rp, rp, vp, rp, vp, vp, rp, vp, vp],
         "wtconv_norm_forward": [nd, rp, rp, vp, rp, vp, vp, vp, rp, rp, vp],
         "wtconv_norm_backward": [nd, rp, rp, vp, rp, vp, vp, vp, rp, rp, rp, rp, vp, rp, vp, vp, vp, sz, vp],
+        "wtconv_causal_workspace_size": [cd], "wtconv_scan_workspace_size": [sd, _i], "wtconv_norm_workspace_size": [nd],
     }
     for name, types in args.items():
         f = getattr(lib, name)
-        f.argtypes, f.restype = types, ctypes.c_int
-    for name, types in (("wtconv_causal_workspace_size", [cd]), ("wtconv_scan_workspace_size", [sd, _i]),
-                        ("wtconv_norm_workspace_size", [nd])):
-        f = getattr(lib, name)
-        f.argtypes, f.restype = types, sz
+        f.argtypes, f.restype = types, sz if name.endswith("size") else ctypes.c_int
+        _call[name] = g = lib[name]
+        g.argtypes, g.restype = [t if t in (sz, _i) else vp for t in types], f.restype
     _bound = lib
     return lib
 
 
-class _on:
-    """The stream of a call, on the inputs' device, which is made the current
-    one (a launch goes to the current device); a stream that was passed in is
-    made current too, so that what is allocated belongs to it."""
-    __slots__ = ("device", "stream", "inside")
+def _entry(name):
+    if _bound is None:
+        load_seq()
+    return _call[name]
 
-    def __init__(self, x, stream):
-        self.device, self.stream, self.inside = x.device, stream, None
 
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError("stream must be on the inputs' device")
-            self.inside = torch.cuda.stream(self.stream)
-            self.inside.__enter__()
-            return self.stream.cuda_stream
-        if self.device.index != torch.cuda.current_device():
-            self.inside = torch.cuda.device(self.device)
-            self.inside.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *e):
-        if self.inside is not None:
-            self.inside.__exit__(*e)
+def _elsewhere(x, stream):
+    """The context of a call on another stream than the current one, or on
+    another device than the current one (a launch goes to the current device):
+    what is allocated then belongs to that stream too."""
+    if stream is None:
+        return torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError("stream must be on the inputs' device")
+    return torch.cuda.stream(stream)
 
 
 def _activation(x, name):
+    """The device of an activation, and the code of its type."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if x.dtype not in _TYPES:
         raise TypeError(f"{name} must be torch.float32 or torch.bfloat16")
+    return x.get_device(), _TYPES[x.dtype]
 
 
-def _tensor(t, name, shape, dtype, like):
-    """t, which has to be a tensor of this shape and type on like's device."""
+def _refuse(t, name, shape, dtype, dev):
+    """Says what is wrong with a tensor that is not of this shape and type on this device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != like.device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the inputs' device")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _dense(t, name, shape, dtype, like):
+def _dense(t, name, shape, dtype, dev):
     """The address of a contiguous tensor (None: NULL)."""
     if t is None:
         return None
-    if not _tensor(t, name, shape, dtype, like).is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
-def _rows(t, name, shape, dtype, like, inner=1):
+_pack_rows = struct.Struct("Pqq").pack
+
+
+def _rows(t, name, shape, dtype, dev, inner=1):
     """A [B, T, ...] or (single token) [B, ...] tensor as the library's rows;
     `inner`: the number of last dimensions that make up a row."""
     if t is None:
         return None
-    _tensor(t, name, shape, dtype, like)
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev)
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1 or inner == 2 and s[-2] != shape[-1] and shape[-2] != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension" + ("s" if inner == 2 else ""))
-    return Rows(t.data_ptr(), s[0], s[1] if len(s) > inner + 1 else 0)
+    return _pack_rows(t.data_ptr(), s[0], s[1] if len(s) > inner + 1 else 0)
 
 
 def _empty(shape, dtype, like):
@@ -152,13 +151,16 @@ def _workspace(need, ws, like):
 
 
 # ---------------------------------------------------------- causal convolution
-def _causal(x, w, silu, T):
-    _activation(x, "x")
+_pack_causal = struct.Struct("6i").pack
+
+
+def _causal(x, w, silu, T, io):
+    """The descriptor, the taps and the shape of the state."""
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must have shape [C, k]")
     B, C = x.shape[0], x.shape[-1]
     k = w.shape[1]
-    return CausalDesc(B, T, C, k, _TYPES[x.dtype], int(bool(silu))), (B, k - 1, C)
+    return _pack_causal(B, T, C, k, io, bool(silu)), k, (B, k - 1, C)
 
 
 def causal_forward(x, w, b=None, silu=True, state=None, lengths=None, y=None, state_out=None, stream=None):
@@ -167,18 +169,20 @@ def causal_forward(x, w, b=None, silu=True, state=None, lengths=None, y=None, st
     y[t] = silu(b + sum_j w[:, j] x[t - (k-1) + j]); x [B, T, C], w [C, k], b [C];
     state [B, k-1, C]: the inputs before the first token (None: zeros);
     state_out: the last k-1 inputs, to go on from (may be `state` itself)."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return causal_forward(x, w, b, silu, state, lengths, y, state_out)
     if x.dim() != 3:
         raise ValueError("x must have shape [B, T, C]")
-    desc, held = _causal(x, w, silu, x.shape[1])
+    desc, k, held = _causal(x, w, silu, x.shape[1], code)
     f32, io, C = torch.float32, x.dtype, x.shape[2]
-    with _on(x, stream) as st:
-        y = _empty(x.shape, io, x) if y is None else y
-        state_out = _empty(held, io, x) if state_out is None else state_out
-        _check(lib.wtconv_causal_forward(desc, _rows(x, "x", x.shape, io, x), _dense(w, "w", (C, desc.k), f32, x),
-                                         _dense(b, "b", (C,), f32, x), _dense(state, "state", held, io, x),
-                                         _dense(lengths, "lengths", (desc.B,), torch.int32, x), _rows(y, "y", x.shape, io, x),
-                                         _dense(state_out, "state_out", held, io, x), st), "wtconv_causal_forward")
+    y = _empty(x.shape, io, x) if y is None else y
+    state_out = _empty(held, io, x) if state_out is None else state_out
+    _check(_entry("wtconv_causal_forward")(desc, _rows(x, "x", x.shape, io, dev), _dense(w, "w", (C, k), f32, dev),
+                                     _dense(b, "b", (C,), f32, dev), _dense(state, "state", held, io, dev),
+                                     _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev), _rows(y, "y", x.shape, io, dev),
+                                     _dense(state_out, "state_out", held, io, dev), _raw_stream(dev)), "wtconv_causal_forward")
     return y, state_out
 
 
@@ -188,24 +192,26 @@ def causal_backward(x, dy, w, b=None, silu=True, state=None, lengths=None, dstat
 
     grads["dstate"] is that of the state before the pass (None without one);
     grads["db"] is None without a bias."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return causal_backward(x, dy, w, b, silu, state, lengths, dstate, dx, grads, ws)
     if x.dim() != 3:
         raise ValueError("x must have shape [B, T, C]")
-    desc, held = _causal(x, w, silu, x.shape[1])
+    desc, k, held = _causal(x, w, silu, x.shape[1], code)
     f32, io, C = torch.float32, x.dtype, x.shape[2]
-    with _on(x, stream) as st:
-        dx = _empty(x.shape, io, x) if dx is None else dx
-        g = grads if grads is not None else dict(dw=torch.empty_like(w), db=None if b is None else torch.empty_like(b),
-                                                 dstate=None if state is None else torch.empty_like(state))
-        ws, nws = _workspace(lib.wtconv_causal_workspace_size(desc), ws, x)
-        _check(lib.wtconv_causal_backward(desc, _rows(x, "x", x.shape, io, x), _rows(dy, "dy", x.shape, io, x),
-                                          _dense(w, "w", (C, desc.k), f32, x), _dense(b, "b", (C,), f32, x),
-                                          _dense(state, "state", held, io, x),
-                                          _dense(lengths, "lengths", (desc.B,), torch.int32, x),
-                                          _dense(dstate, "dstate", held, io, x), _rows(dx, "dx", x.shape, io, x),
-                                          _dense(g["dw"], "dw", (C, desc.k), f32, x), _dense(g["db"], "db", (C,), f32, x),
-                                          _dense(g["dstate"], "grads['dstate']", held, io, x), ws.data_ptr(), nws, st),
-               "wtconv_causal_backward")
+    dx = _empty(x.shape, io, x) if dx is None else dx
+    g = grads if grads is not None else dict(dw=torch.empty_like(w), db=None if b is None else torch.empty_like(b),
+                                             dstate=None if state is None else torch.empty_like(state))
+    ws, nws = _workspace(_entry("wtconv_causal_workspace_size")(desc), ws, x)
+    _check(_entry("wtconv_causal_backward")(desc, _rows(x, "x", x.shape, io, dev), _rows(dy, "dy", x.shape, io, dev),
+                                      _dense(w, "w", (C, k), f32, dev), _dense(b, "b", (C,), f32, dev),
+                                      _dense(state, "state", held, io, dev),
+                                      _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev),
+                                      _dense(dstate, "dstate", held, io, dev), _rows(dx, "dx", x.shape, io, dev),
+                                      _dense(g["dw"], "dw", (C, k), f32, dev), _dense(g["db"], "db", (C,), f32, dev),
+                                      _dense(g["dstate"], "grads['dstate']", held, io, dev), ws.data_ptr(), nws, _raw_stream(dev)),
+           "wtconv_causal_backward")
     return dx, g
 
 
@@ -213,24 +219,28 @@ def causal_step(x, state, w, b=None, silu=True, active=None, y=None, stream=None
     """One token of every row, y [B, C] of x [B, C]; state [B, k-1, C] is moved
     on in place.  active (int32 [B]): 0 leaves a row's state as it is and its
     output zero."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return causal_step(x, state, w, b, silu, active, y)
     if x.dim() != 2:
         raise ValueError("x must have shape [B, C]")
-    desc, held = _causal(x, w, silu, 1)
+    desc, k, held = _causal(x, w, silu, 1, code)
     f32, io, C = torch.float32, x.dtype, x.shape[1]
-    with _on(x, stream) as st:
-        y = _empty(x.shape, io, x) if y is None else y
-        _check(lib.wtconv_causal_step(desc, _rows(x, "x", x.shape, io, x), _dense(w, "w", (C, desc.k), f32, x),
-                                      _dense(b, "b", (C,), f32, x), _dense(active, "active", (desc.B,), torch.int32, x),
-                                      _rows(y, "y", x.shape, io, x), _dense(state, "state", held, io, x), st),
-               "wtconv_causal_step")
+    y = _empty(x.shape, io, x) if y is None else y
+    _check(_entry("wtconv_causal_step")(desc, _rows(x, "x", x.shape, io, dev), _dense(w, "w", (C, k), f32, dev),
+                                  _dense(b, "b", (C,), f32, dev), _dense(active, "active", (x.shape[0],), torch.int32, dev),
+                                  _rows(y, "y", x.shape, io, dev), _dense(state, "state", held, io, dev), _raw_stream(dev)),
+           "wtconv_causal_step")
     return y
 
 
 # ------------------------------------------------------------------------ scan
-def _scan(x, a, b, softplus, T):
-    """The descriptor and the shape of b and c (groups may be left out)."""
-    _activation(x, "x")
+_pack_scan = struct.Struct("7i").pack
+
+
+def _scan(x, a, b, softplus, T, io):
+    """The descriptor, the states and the shape of b and c (groups may be left out)."""
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a must have shape [C, N]")
     lead = x.dim() - 1
@@ -239,7 +249,7 @@ def _scan(x, a, b, softplus, T):
     N = a.shape[1]
     G = b.shape[-2] if b.dim() == lead + 2 else 1
     inner = (G, N) if b.dim() == lead + 2 else (N,)
-    return ScanDesc(x.shape[0], T, x.shape[-1], N, G, _TYPES[x.dtype], int(bool(softplus))), x.shape[:lead] + inner
+    return _pack_scan(x.shape[0], T, x.shape[-1], N, G, io, bool(softplus)), N, x.shape[:lead] + inner
 
 
 def scan_forward(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=True, state=None, lengths=None, y=None,
@@ -250,25 +260,27 @@ def scan_forward(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus=True, st
     y = (c . h + d x) silu(z).  x, dt, z [B, T, C]; a [C, N] fp32; b, c
     [B, T, N], or [B, T, G, N] for G groups of channels; d, dt_bias [C] fp32;
     state, state_out [B, C, N] fp32 (state_out may be `state` itself)."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return scan_forward(x, dt, a, b, c, d, z, dt_bias, softplus, state, lengths, y, state_out, ws)
     if x.dim() != 3:
         raise ValueError("x must have shape [B, T, C]")
-    desc, bc = _scan(x, a, b, softplus, x.shape[1])
+    desc, N, bc = _scan(x, a, b, softplus, x.shape[1], code)
     f32, io, S, C, inner = torch.float32, x.dtype, x.shape, x.shape[2], len(bc) - 2
-    held = (desc.B, C, desc.N)
-    with _on(x, stream) as st:
-        y = _empty(S, io, x) if y is None else y
-        state_out = _empty(held, f32, x) if state_out is None else state_out
-        need = lib.wtconv_scan_workspace_size(desc, 0)
-        ws, nws = _workspace(need, ws, x) if need or ws is not None else (None, 0)
-        _check(lib.wtconv_scan_forward(desc, _rows(x, "x", S, io, x), _rows(dt, "dt", S, io, x),
-                                       _dense(a, "a", (C, desc.N), f32, x), _rows(b, "b", bc, io, x, inner),
-                                       _rows(c, "c", bc, io, x, inner), _dense(d, "d", (C,), f32, x),
-                                       _rows(z, "z", S, io, x), _dense(dt_bias, "dt_bias", (C,), f32, x),
-                                       _dense(state, "state", held, f32, x),
-                                       _dense(lengths, "lengths", (desc.B,), torch.int32, x), _rows(y, "y", S, io, x),
-                                       _dense(state_out, "state_out", held, f32, x), None if ws is None else ws.data_ptr(),
-                                       nws, st), "wtconv_scan_forward")
+    held = (x.shape[0], C, N)
+    y = _empty(S, io, x) if y is None else y
+    state_out = _empty(held, f32, x) if state_out is None else state_out
+    need = _entry("wtconv_scan_workspace_size")(desc, 0)
+    ws, nws = _workspace(need, ws, x) if need or ws is not None else (None, 0)
+    _check(_entry("wtconv_scan_forward")(desc, _rows(x, "x", S, io, dev), _rows(dt, "dt", S, io, dev),
+                                   _dense(a, "a", (C, N), f32, dev), _rows(b, "b", bc, io, dev, inner),
+                                   _rows(c, "c", bc, io, dev, inner), _dense(d, "d", (C,), f32, dev),
+                                   _rows(z, "z", S, io, dev), _dense(dt_bias, "dt_bias", (C,), f32, dev),
+                                   _dense(state, "state", held, f32, dev),
+                                   _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev), _rows(y, "y", S, io, dev),
+                                   _dense(state_out, "state_out", held, f32, dev), None if ws is None else ws.data_ptr(),
+                                   nws, _raw_stream(dev)), "wtconv_scan_forward")
     return y, state_out
 
 
@@ -277,33 +289,35 @@ def scan_backward(x, dt, a, b, c, dy, d=None, z=None, dt_bias=None, softplus=Tru
     """Gradients of <y, dy> + <state_out, dstate>: dict dx, ddt, da, db, dc, dd,
     dz, ddt_bias, dstate (the last for the state before the pass), None for
     inputs that are not given."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return scan_backward(x, dt, a, b, c, dy, d, z, dt_bias, softplus, state, lengths, dstate, grads, ws)
     if x.dim() != 3:
         raise ValueError("x must have shape [B, T, C]")
-    desc, bc = _scan(x, a, b, softplus, x.shape[1])
+    desc, N, bc = _scan(x, a, b, softplus, x.shape[1], code)
     f32, io, S, C, inner = torch.float32, x.dtype, x.shape, x.shape[2], len(bc) - 2
-    held = (desc.B, C, desc.N)
-    with _on(x, stream) as st:
-        g = grads
-        if g is None:
-            new = lambda t, shape, dtype: None if t is None else _empty(shape, dtype, x)
-            g = dict(dx=_empty(S, io, x), ddt=_empty(S, io, x), da=_empty((C, desc.N), f32, x), db=_empty(bc, io, x),
-                     dc=_empty(bc, io, x), dd=new(d, (C,), f32), dz=new(z, S, io), ddt_bias=new(dt_bias, (C,), f32),
-                     dstate=new(state, held, f32))
-        ws, nws = _workspace(lib.wtconv_scan_workspace_size(desc, 1), ws, x)
-        _check(lib.wtconv_scan_backward(desc, _rows(x, "x", S, io, x), _rows(dt, "dt", S, io, x),
-                                        _dense(a, "a", (C, desc.N), f32, x), _rows(b, "b", bc, io, x, inner),
-                                        _rows(c, "c", bc, io, x, inner), _dense(d, "d", (C,), f32, x),
-                                        _rows(z, "z", S, io, x), _dense(dt_bias, "dt_bias", (C,), f32, x),
-                                        _dense(state, "state", held, f32, x),
-                                        _dense(lengths, "lengths", (desc.B,), torch.int32, x),
-                                        _rows(dy, "dy", S, io, x), _dense(dstate, "dstate", held, f32, x),
-                                        _rows(g["dx"], "dx", S, io, x), _rows(g["ddt"], "ddt", S, io, x),
-                                        _dense(g["da"], "da", (C, desc.N), f32, x), _rows(g["db"], "db", bc, io, x, inner),
-                                        _rows(g["dc"], "dc", bc, io, x, inner), _dense(g["dd"], "dd", (C,), f32, x),
-                                        _rows(g["dz"], "dz", S, io, x), _dense(g["ddt_bias"], "ddt_bias", (C,), f32, x),
-                                        _dense(g["dstate"], "grads['dstate']", held, f32, x), ws.data_ptr(), nws, st),
-               "wtconv_scan_backward")
+    held = (x.shape[0], C, N)
+    g = grads
+    if g is None:
+        new = lambda t, shape, dtype: None if t is None else _empty(shape, dtype, x)
+        g = dict(dx=_empty(S, io, x), ddt=_empty(S, io, x), da=_empty((C, N), f32, x), db=_empty(bc, io, x),
+                 dc=_empty(bc, io, x), dd=new(d, (C,), f32), dz=new(z, S, io), ddt_bias=new(dt_bias, (C,), f32),
+                 dstate=new(state, held, f32))
+    ws, nws = _workspace(_entry("wtconv_scan_workspace_size")(desc, 1), ws, x)
+    _check(_entry("wtconv_scan_backward")(desc, _rows(x, "x", S, io, dev), _rows(dt, "dt", S, io, dev),
+                                    _dense(a, "a", (C, N), f32, dev), _rows(b, "b", bc, io, dev, inner),
+                                    _rows(c, "c", bc, io, dev, inner), _dense(d, "d", (C,), f32, dev),
+                                    _rows(z, "z", S, io, dev), _dense(dt_bias, "dt_bias", (C,), f32, dev),
+                                    _dense(state, "state", held, f32, dev),
+                                    _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev),
+                                    _rows(dy, "dy", S, io, dev), _dense(dstate, "dstate", held, f32, dev),
+                                    _rows(g["dx"], "dx", S, io, dev), _rows(g["ddt"], "ddt", S, io, dev),
+                                    _dense(g["da"], "da", (C, N), f32, dev), _rows(g["db"], "db", bc, io, dev, inner),
+                                    _rows(g["dc"], "dc", bc, io, dev, inner), _dense(g["dd"], "dd", (C,), f32, dev),
+                                    _rows(g["dz"], "dz", S, io, dev), _dense(g["ddt_bias"], "ddt_bias", (C,), f32, dev),
+                                    _dense(g["dstate"], "grads['dstate']", held, f32, dev), ws.data_ptr(), nws, _raw_stream(dev)),
+           "wtconv_scan_backward")
     return g
 
 
@@ -311,32 +325,36 @@ def scan_step(x, dt, state, a, b, c, d=None, z=None, dt_bias=None, softplus=True
     """One token of every row, y [B, C] of x, dt, z [B, C] and b, c [B, N] or
     [B, G, N]; state [B, C, N] fp32 is moved on in place.  active (int32 [B]):
     0 leaves a row's state as it is and its output zero."""
-    lib = load_seq()
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return scan_step(x, dt, state, a, b, c, d, z, dt_bias, softplus, active, y)
     if x.dim() != 2:
         raise ValueError("x must have shape [B, C]")
-    desc, bc = _scan(x, a, b, softplus, 1)
+    desc, N, bc = _scan(x, a, b, softplus, 1, code)
     f32, io, S, C, inner = torch.float32, x.dtype, x.shape, x.shape[1], len(bc) - 1
-    with _on(x, stream) as st:
-        y = _empty(S, io, x) if y is None else y
-        _check(lib.wtconv_scan_step(desc, _rows(x, "x", S, io, x), _rows(dt, "dt", S, io, x),
-                                    _dense(a, "a", (C, desc.N), f32, x), _rows(b, "b", bc, io, x, inner),
-                                    _rows(c, "c", bc, io, x, inner), _dense(d, "d", (C,), f32, x), _rows(z, "z", S, io, x),
-                                    _dense(dt_bias, "dt_bias", (C,), f32, x),
-                                    _dense(active, "active", (desc.B,), torch.int32, x), _rows(y, "y", S, io, x),
-                                    _dense(state, "state", (desc.B, C, desc.N), f32, x), st), "wtconv_scan_step")
+    y = _empty(S, io, x) if y is None else y
+    _check(_entry("wtconv_scan_step")(desc, _rows(x, "x", S, io, dev), _rows(dt, "dt", S, io, dev),
+                                _dense(a, "a", (C, N), f32, dev), _rows(b, "b", bc, io, dev, inner),
+                                _rows(c, "c", bc, io, dev, inner), _dense(d, "d", (C,), f32, dev), _rows(z, "z", S, io, dev),
+                                _dense(dt_bias, "dt_bias", (C,), f32, dev),
+                                _dense(active, "active", (x.shape[0],), torch.int32, dev), _rows(y, "y", S, io, dev),
+                                _dense(state, "state", (x.shape[0], C, N), f32, dev), _raw_stream(dev)), "wtconv_scan_step")
     return y
 
 
 # ------------------------------------------------------------------------ norm
-def _norm(x, res, eps):
-    _activation(x, "x")
+_pack_norm = struct.Struct("5if").pack
+
+
+def _norm(x, res, eps, io):
+    """The descriptor and the residual's type."""
     if x.dim() not in (2, 3):
         raise ValueError("x must have shape [B, T, C] or [B, C]")
-    if res is not None:
-        _activation(res, "res")
+    res_io = io if res is None else _activation(res, "res")[1]
     T = x.shape[1] if x.dim() == 3 else 1
     rt = x.dtype if res is None else res.dtype
-    return NormDesc(x.shape[0], T, x.shape[-1], _TYPES[x.dtype], _TYPES[rt], eps), rt
+    return _pack_norm(x.shape[0], T, x.shape[-1], io, res_io, eps), rt
 
 
 def norm_forward(x, w=None, gate=None, res=None, scale=None, w_res=None, eps=1e-6, lengths=None, y=None, res_out=None,
@@ -349,19 +367,21 @@ def norm_forward(x, w=None, gate=None, res=None, scale=None, w_res=None, eps=1e-
     may be left out; without res y = v and res_out is None, without w_res y is
     None.  x, gate [B, T, C] or [B, C]; res in fp32 or bf16, whatever x is;
     w, scale, w_res [C] fp32."""
-    lib = load_seq()
-    desc, rt = _norm(x, res, eps)
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return norm_forward(x, w, gate, res, scale, w_res, eps, lengths, y, res_out)
+    desc, rt = _norm(x, res, eps, code)
     f32, io, S, V = torch.float32, x.dtype, x.shape, (x.shape[-1],)
-    with _on(x, stream) as st:
-        if y is None and (res is None or w_res is not None):
-            y = _empty(S, io, x)
-        if res_out is None and res is not None:
-            res_out = _empty(S, rt, x)
-        _check(lib.wtconv_norm_forward(desc, _rows(x, "x", S, io, x), _rows(gate, "gate", S, io, x), _dense(w, "w", V, f32, x),
-                                       _rows(res, "res", S, rt, x), _dense(scale, "scale", V, f32, x),
-                                       _dense(w_res, "w_res", V, f32, x),
-                                       _dense(lengths, "lengths", (desc.B,), torch.int32, x), _rows(y, "y", S, io, x),
-                                       _rows(res_out, "res_out", S, rt, x), st), "wtconv_norm_forward")
+    if y is None and (res is None or w_res is not None):
+        y = _empty(S, io, x)
+    if res_out is None and res is not None:
+        res_out = _empty(S, rt, x)
+    _check(_entry("wtconv_norm_forward")(desc, _rows(x, "x", S, io, dev), _rows(gate, "gate", S, io, dev), _dense(w, "w", V, f32, dev),
+                                   _rows(res, "res", S, rt, dev), _dense(scale, "scale", V, f32, dev),
+                                   _dense(w_res, "w_res", V, f32, dev),
+                                   _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev), _rows(y, "y", S, io, dev),
+                                   _rows(res_out, "res_out", S, rt, dev), _raw_stream(dev)), "wtconv_norm_forward")
     return y, res_out
 
 
@@ -370,23 +390,25 @@ def norm_backward(x, dy=None, w=None, gate=None, res=None, scale=None, w_res=Non
     """Gradients of <y, dy> + <res_out, dres>: dict dx, dgate, dw, dres (of the
     residual that came in), dscale, dw_res, None for inputs that are not given.
     dy is None exactly where the forward pass gives no y; dres None is zero."""
-    lib = load_seq()
-    desc, rt = _norm(x, res, eps)
+    dev, code = _activation(x, "x")
+    if stream is not None or dev != _current_device():
+        with _elsewhere(x, stream):
+            return norm_backward(x, dy, w, gate, res, scale, w_res, dres, eps, lengths, grads, ws)
+    desc, rt = _norm(x, res, eps, code)
     f32, io, S, V = torch.float32, x.dtype, x.shape, (x.shape[-1],)
-    with _on(x, stream) as st:
-        g = grads
-        if g is None:
-            new = lambda t, shape, dtype: None if t is None else _empty(shape, dtype, x)
-            g = dict(dx=_empty(S, io, x), dgate=new(gate, S, io), dw=new(w, V, f32), dres=new(res, S, rt),
-                     dscale=new(scale, V, f32), dw_res=new(w_res, V, f32))
-        ws, nws = _workspace(lib.wtconv_norm_workspace_size(desc), ws, x)
-        _check(lib.wtconv_norm_backward(desc, _rows(x, "x", S, io, x), _rows(gate, "gate", S, io, x),
-                                        _dense(w, "w", V, f32, x), _rows(res, "res", S, rt, x),
-                                        _dense(scale, "scale", V, f32, x), _dense(w_res, "w_res", V, f32, x),
-                                        _dense(lengths, "lengths", (desc.B,), torch.int32, x), _rows(dy, "dy", S, io, x),
-                                        _rows(dres, "dres", S, rt, x), _rows(g["dx"], "dx", S, io, x),
-                                        _rows(g["dgate"], "dgate", S, io, x), _dense(g["dw"], "dw", V, f32, x),
-                                        _rows(g["dres"], "dres", S, rt, x), _dense(g["dscale"], "dscale", V, f32, x),
-                                        _dense(g["dw_res"], "dw_res", V, f32, x), ws.data_ptr(), nws, st),
-               "wtconv_norm_backward")
+    g = grads
+    if g is None:
+        new = lambda t, shape, dtype: None if t is None else _empty(shape, dtype, x)
+        g = dict(dx=_empty(S, io, x), dgate=new(gate, S, io), dw=new(w, V, f32), dres=new(res, S, rt),
+                 dscale=new(scale, V, f32), dw_res=new(w_res, V, f32))
+    ws, nws = _workspace(_entry("wtconv_norm_workspace_size")(desc), ws, x)
+    _check(_entry("wtconv_norm_backward")(desc, _rows(x, "x", S, io, dev), _rows(gate, "gate", S, io, dev),
+                                    _dense(w, "w", V, f32, dev), _rows(res, "res", S, rt, dev),
+                                    _dense(scale, "scale", V, f32, dev), _dense(w_res, "w_res", V, f32, dev),
+                                    _dense(lengths, "lengths", (x.shape[0],), torch.int32, dev), _rows(dy, "dy", S, io, dev),
+                                    _rows(dres, "dres", S, rt, dev), _rows(g["dx"], "dx", S, io, dev),
+                                    _rows(g["dgate"], "dgate", S, io, dev), _dense(g["dw"], "dw", V, f32, dev),
+                                    _rows(g["dres"], "dres", S, rt, dev), _dense(g["dscale"], "dscale", V, f32, dev),
+                                    _dense(g["dw_res"], "dw_res", V, f32, dev), ws.data_ptr(), nws, _raw_stream(dev)),
+           "wtconv_norm_backward")
     return g

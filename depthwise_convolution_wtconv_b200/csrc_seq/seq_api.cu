@@ -579,9 +579,15 @@ wtconv_status wtconv_scan_step(const wtconv_scan_desc* desc, const wtconv_rows* 
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
     p.y = rows_of<IO>(y);
     p.state_out = state;
-    const long long blocks = ceil_div((long long)p.B * p.C * 4, 128);
+    p.blocks = (int)ceil_div(p.C, 32);
+    const long long blocks = (long long)p.blocks * p.B;
     if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
-    scan_step_kernel<IO><<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(p, active);
+    const size_t e = sizeof(IO);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.N % 4 == 0 && wide(a, 4, 4) && wide(state, 4, 4) && wide(b, 4, e, p.B, 1) && wide(c, 4, e, p.B, 1))
+      scan_step_kernel<IO, true><<<(unsigned)blocks, 128, 0, st>>>(p, active);
+    else
+      scan_step_kernel<IO, false><<<(unsigned)blocks, 128, 0, st>>>(p, active);
     return launched();
   });
 }

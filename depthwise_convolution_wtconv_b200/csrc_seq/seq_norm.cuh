@@ -230,13 +230,13 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
 //   dx = du silu(gate)   dgate = du x silu'(gate)
 template <typename IO, typename RES, int V, int NV>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES> a) {
-  constexpr bool AHEAD = V * NV <= 8;
+  constexpr bool AHEAD = V * NV <= 8, KEEP = AHEAD;
   constexpr int P = Vals<V>::P;
   __shared__ __align__(16) float s1[2][1][NORM_WARPS], s2[2][2][NORM_WARPS], s3[2][1][NORM_WARPS];
   for (int i = threadIdx.x; i < 2 * NORM_WARPS; i += blockDim.x) s1[0][0][i] = s2[0][0][i] = s2[1][0][i] = s3[0][0][i] = 0.f;
   __syncthreads();
   const float per = 1.f / a.C;
-  const Params<V, NV, AHEAD> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
+  const Params<V, NV, KEEP> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
   Vals<V> aw[NV], as[NV], ar[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) aw[i].zero(), as[i].zero(), ar[i].zero();

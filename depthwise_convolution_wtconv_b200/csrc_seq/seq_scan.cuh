@@ -790,29 +790,48 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
   }
 }
 
-// One token of every row: four threads share a channel's states, each a
-// quarter of them, and join their sums over the four.
-template <typename IO>
-__global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs<IO> p, const int* __restrict__ active) {
-  const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
-  const long long ch = id >> 2;
-  const int q = (int)(id & 3);
-  const int b = (int)min(ch / p.C, (long long)p.B - 1), c = (int)(ch % p.C);
-  const bool on = ch < (long long)p.B * p.C;
-  const bool live = on && (!active || __ldg(active + b));
-  float y = 0.f, x = 0.f;
+// One token of every row: four threads share a channel's states and join their
+// sums over the four.  With VEC, four states at a time: the state, 8 bytes a
+// state of traffic where everything else is less than one, goes in 16-byte
+// accesses, whole sectors of a row at once.
+template <typename IO, bool VEC>
+__global__ void __launch_bounds__(128) scan_step_kernel(const ScanArgs<IO> p, const int* __restrict__ active) {
+  const int blk = blockIdx.x % p.blocks, b = blockIdx.x / p.blocks, q = threadIdx.x & 3;
+  const int c = blk * 32 + (threadIdx.x >> 2), N = p.N;
+  const bool on = c < p.C, live = on && (!active || __ldg(active + b));
+  float y = 0.f, x = 0.f, z = 0.f;
   if (live) {
-    const int N = p.N, g = c / (p.C / p.G);
-    x = to_f<IO>(p.x.at(b, 0)[c]);
-    float delta = to_f<IO>(p.dt.at(b, 0)[c]) + (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f);
-    if (p.softplus) delta = softplus(delta);
-    const IO* bv = p.b.at(b, 0) + (long long)g * N;
-    const IO* cv = p.c.at(b, 0) + (long long)g * N;
-    float* h = p.state_out + ((long long)b * p.C + c) * N;
-    for (int n = q; n < N; n += 4) {
-      const float v = fmaf(exp2_approx(delta * (__ldg(p.a + (long long)c * N + n) * LOG2E)), h[n], delta * x * to_f<IO>(bv[n]));
-      h[n] = v;
-      y = fmaf(to_f<IO>(cv[n]), v, y);
+    const long long g = c / (p.C / p.G);
+    const IO* const bv = p.b.at(b, 0) + g * N;
+    const IO* const cv = p.c.at(b, 0) + g * N;
+    const float* const av = p.a + (long long)c * N;
+    float* const h = p.state_out + ((long long)b * p.C + c) * N;
+    x = to_f<IO>(__ldg(p.x.at(b, 0) + c));
+    if (p.z.p) z = to_f<IO>(__ldg(p.z.at(b, 0) + c));
+    float delta = to_f<IO>(__ldg(p.dt.at(b, 0) + c)) + (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f);
+    auto softened = [&] { return p.softplus ? softplus(delta) : delta; };
+    if constexpr (VEC) {
+      for (int n = q * 4; n < N; n += 16) {
+        float hv[4], a[4], bf[4], cf[4];
+        load_pack<float, 4>(h + n, hv);
+        load_pack<float, 4>(av + n, a);
+        load_pack<IO, 4>(bv + n, bf);
+        load_pack<IO, 4>(cv + n, cf);
+        const float d = softened();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hv[i] = fmaf(exp2_approx(fmaf(d, a[i] * LOG2E, EXP_BIAS)), hv[i], d * x * bf[i]);
+          y = fmaf(cf[i], hv[i], y);
+        }
+        store_pack<float, 4>(h + n, hv);
+      }
+    } else {
+      const float d = softened();
+      for (int n = q; n < N; n += 4) {
+        const float v = fmaf(exp2_approx(fmaf(d, __ldg(av + n) * LOG2E, EXP_BIAS)), h[n], d * x * to_f<IO>(bv[n]));
+        h[n] = v;
+        y = fmaf(to_f<IO>(cv[n]), v, y);
+      }
     }
   }
   y += __shfl_xor_sync(0xffffffffu, y, 1);
@@ -820,10 +839,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs<IO> p, const in
   if (!on || q) return;
   if (live) {
     y = fmaf(p.d ? __ldg(p.d + c) : 0.f, x, y);
-    if (p.z.p) {
-      const float z = to_f<IO>(p.z.at(b, 0)[c]);
-      y *= z * sigmoid(z);
-    }
+    if (p.z.p) y *= z * sigmoid(z);
   }
   p.y.at(b, 0)[c] = from_f<IO>(y);
 }
