@@ -72,34 +72,35 @@ template <typename IO> __device__ __forceinline__ IO* row_at(const Rows<IO>& r, 
 
 // The fp32 parameters of a thread's channels: kept in registers, or loaded
 // where they are used.
+// (one where there is none; the product of two)
 template <int V, int NV, bool KEEP> struct Params {
-  const float* p;
+  const float *p, *p2;
   Vals<V> kept[KEEP ? NV : 1];
-  __device__ __forceinline__ Vals<V> load(int c, float none) const {
+  __device__ __forceinline__ Vals<V> load(int c) const {
     float f[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = p ? __ldg(p + c + k) : none;
+    for (int k = 0; k < V; ++k) f[k] = (p ? __ldg(p + c + k) : 1.f) * (p2 ? __ldg(p2 + c + k) : 1.f);
     Vals<V> v;
     v.set(f);
     return v;
   }
-  __device__ __forceinline__ Params(const float* from, int C, float none) : p(from) {
+  __device__ __forceinline__ Params(const float* p, const float* p2, int C) : p(p), p2(p2) {
     if constexpr (KEEP) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c < C)
-          kept[i] = load(c, none);
+          kept[i] = load(c);
         else
           kept[i].zero();
       }
     }
   }
-  __device__ __forceinline__ Vals<V> get(int i, int c, float none) const {
+  __device__ __forceinline__ Vals<V> get(int i, int c) const {
     if constexpr (KEEP)
       return kept[i];
     else
-      return load(c, none);
+      return load(c);
   }
 };
 
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
   for (int i = threadIdx.x; i < 4 * NORM_WARPS; i += blockDim.x) sums[0][0][0][i] = 0.f;
   __syncthreads();
   const float per = 1.f / a.C;
-  const Params<V, NV, AHEAD> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
+  const Params<V, NV, AHEAD> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);  // res_out = res + sw u n1
   RowIn<IO, V, NV> x, gate;
   RowIn<RES, V, NV> res;
   NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
       }
       continue;
     }
+    float n1 = 1.f, n2 = 1.f;
     if (a.w) {
       float q[1] = {0.f};
 #pragma unroll
@@ -177,44 +179,34 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
 #pragma unroll
         for (int k = 0; k < V; ++k) q[0] = fmaf(u[i][k], u[i][k], q[0]);
       block_sum(q, sums[turn][0]);
-      const float n1 = rsqrtf(fmaf(q[0], per, a.eps));
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) continue;
-        float f[V];
-        w.get(i, c, 1.f).get(f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) u[i][k] *= n1 * f[k];
-      }
+      n1 = rsqrtf(fmaf(q[0], per, a.eps));
     }
-    float n2 = 1.f;
-    if (a.res.p) {
-      float q[1] = {0.f};
+    float q[1] = {0.f};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) continue;
-        float f[V];
-        scale.get(i, c, 1.f).get(f);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c >= a.C) continue;
+      float f[V];
+      sw.get(i, c).get(f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          u[i][k] = fmaf(f[k], u[i][k], r[i][k]);
-          q[0] = fmaf(u[i][k], u[i][k], q[0]);
-        }
-        store_pack<RES, V>(row_at(a.res_out, b, t) + c, u[i]);
+      for (int k = 0; k < V; ++k) {
+        u[i][k] = fmaf(f[k], u[i][k] * n1, r[i][k]);
+        q[0] = fmaf(u[i][k], u[i][k], q[0]);
       }
-      if (!a.w_res) continue;
+      if (a.res.p) store_pack<RES, V>(row_at(a.res_out, b, t) + c, u[i]);
+    }
+    if (a.w_res) {
       block_sum(q, sums[turn][1]);
       n2 = rsqrtf(fmaf(q[0], per, a.eps));
     }
+    if (!a.y.p) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
       if (c >= a.C) continue;
       float f[V];
       if (a.w_res) {
-        w_res.get(i, c, 1.f).get(f);
+        w_res.get(i, c).get(f);
 #pragma unroll
         for (int k = 0; k < V; ++k) u[i][k] *= n2 * f[k];
       }
@@ -225,9 +217,11 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
 
 // Gradients.  With t = dy w_res:
 //   dr = dres_out + n2 t - r n2^3 mean(r t)      dw_res = sum dy r n2
-//   dres = dr   dscale = sum dr v   q = dr scale (or dy, without res)
-//   dw = sum q u n1   du = n1 q w - u n1^3 mean(u q w)
+//   dres = dr   S = sum dr u n1   dscale = S w   dw = S scale
+//   du = n1 q - u n1^3 mean(u q), q = dr scale w
 //   dx = du silu(gate)   dgate = du x silu'(gate)
+// Without res, dr is dy.  dscale and dw share the sum over the rows, and scale
+// and w are only needed as their product until the end.
 template <typename IO, typename RES, int V, int NV>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES> a) {
   constexpr bool AHEAD = V * NV <= 8, KEEP = AHEAD;
@@ -236,10 +230,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
   for (int i = threadIdx.x; i < 2 * NORM_WARPS; i += blockDim.x) s1[0][0][i] = s2[0][0][i] = s2[1][0][i] = s3[0][0][i] = 0.f;
   __syncthreads();
   const float per = 1.f / a.C;
-  const Params<V, NV, KEEP> w(a.w, a.C, 1.f), scale(a.scale, a.C, 1.f), w_res(a.w_res, a.C, 1.f);
-  Vals<V> aw[NV], as[NV], ar[NV];
+  const Params<V, NV, KEEP> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);
+  Vals<V> as[NV], ar[NV];  // S and dw_res
 #pragma unroll
-  for (int i = 0; i < NV; ++i) aw[i].zero(), as[i].zero(), ar[i].zero();
+  for (int i = 0; i < NV; ++i) as[i].zero(), ar[i].zero();
   RowIn<IO, V, NV> x, gate, dy;
   RowIn<RES, V, NV> res, dres;
   NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
@@ -271,7 +265,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
     const bool live = t < row_length(a.lengths, b, a.T);
     if (!AHEAD) load(), then.next();
     // u = x act; act = silu(gate) and xd = x silu'(gate) wait for the end
-    Vals<V> u[NV], act[NV], xd[NV], r[NV], q[NV], g[NV];
+    Vals<V> u[NV], act[NV], xd[NV], r[NV], q[NV], g[NV];  // q: dy, then dr, then dr scale w
     f32x2 uu = 0;
     if (live) {
 #pragma unroll
@@ -323,10 +317,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c >= a.C) continue;
-        const Vals<V> fs = scale.get(i, c, 1.f), fw = w.get(i, c, 1.f), fr = w_res.get(i, c, 1.f);
+        const Vals<V> f = sw.get(i, c), fr = w_res.get(i, c);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          r[i].p[k] = fma2(fs.p[k], mul2(u[i].p[k], fw.p[k]), r[i].p[k]);
+          r[i].p[k] = fma2(f.p[k], u[i].p[k], r[i].p[k]);
           rr = fma2(r[i].p[k], r[i].p[k], rr);
           rt = fma2(r[i].p[k], mul2(q[i].p[k], fr.p[k]), rt);
         }
@@ -342,34 +336,32 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
       for (int i = 0; i < NV; ++i) {
         const int c = (i * blockDim.x + threadIdx.x) * V;
         if (c >= a.C) continue;
-        const Vals<V> fs = scale.get(i, c, 1.f), fw = w.get(i, c, 1.f), fr = w_res.get(i, c, 1.f);
+        const Vals<V> fr = w_res.get(i, c);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          const f32x2 qn = mul2(q[i].p[k], twice(n2));
+          const f32x2 qn = mul2(q[i].p[k], twice(n2));  // zero without w_res, and m too
           ar[i].p[k] = fma2(qn, r[i].p[k], ar[i].p[k]);
-          g[i].p[k] = fma2(r[i].p[k], twice(m), fma2(qn, fr.p[k], g[i].p[k]));  // as it was, without w_res
-          as[i].p[k] = fma2(g[i].p[k], mul2(u[i].p[k], fw.p[k]), as[i].p[k]);
-          q[i].p[k] = mul2(g[i].p[k], fs.p[k]);
+          q[i].p[k] = fma2(r[i].p[k], twice(m), fma2(qn, fr.p[k], g[i].p[k]));
         }
         float f[V];
-        g[i].get(f);
+        q[i].get(f);
         store_pack<RES, V>(row_at(a.dres, b, t) + c, f);
       }
     }
-    if (a.w) {
-      f32x2 uq = 0;
+    f32x2 uq = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) continue;
-        const Vals<V> fw = w.get(i, c, 1.f);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c >= a.C) continue;
+      const Vals<V> f = sw.get(i, c);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          aw[i].p[k] = fma2(q[i].p[k], u[i].p[k], aw[i].p[k]);
-          q[i].p[k] = mul2(q[i].p[k], fw.p[k]);
-          uq = fma2(u[i].p[k], q[i].p[k], uq);
-        }
+      for (int k = 0; k < P; ++k) {
+        as[i].p[k] = fma2(q[i].p[k], u[i].p[k], as[i].p[k]);
+        q[i].p[k] = mul2(q[i].p[k], f.p[k]);
+        uq = fma2(u[i].p[k], q[i].p[k], uq);
       }
+    }
+    if (a.w) {
       float s[1] = {total(uq)};
       block_sum(s, s3[turn]);
       const float m = -s[0] * per * n1;
@@ -401,10 +393,14 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
     const int c = (i * blockDim.x + threadIdx.x) * V;
     if (c >= a.C) continue;
     float* p = a.part + (long long)blockIdx.x * 3 * a.C + c;
-    float f0[V], f1[V], f2[V];
-    aw[i].get(f0), as[i].get(f1), ar[i].get(f2);
+    float f1[V], f2[V];
+    as[i].get(f1), ar[i].get(f2);
 #pragma unroll
-    for (int k = 0; k < V; ++k) p[k] = f0[k], p[a.C + k] = f1[k], p[2 * a.C + k] = f2[k];
+    for (int k = 0; k < V; ++k) {
+      p[k] = f1[k] * (a.scale ? __ldg(a.scale + c + k) : 1.f);
+      p[a.C + k] = f1[k] * (a.w ? __ldg(a.w + c + k) : 1.f);
+      p[2 * a.C + k] = f2[k];
+    }
   }
 }
 
