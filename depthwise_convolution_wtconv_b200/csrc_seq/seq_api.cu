@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "seq_causal.cuh"
 #include "seq_common.cuh"
@@ -380,9 +381,10 @@ template <int V, typename F> wtconv_status norm_shape(int C, F f) {
   return f(Int<V>(), Int<N3>(), threads(N3));
 }
 
-template <typename IO, typename RES, typename F> wtconv_status norm_variant(int C, bool vec, F f) {
-  constexpr int V = sizeof(IO) == 2 ? 8 : 4;
-  return vec ? norm_shape<V>(C, f) : norm_shape<1>(C, f);
+// ... and whether chunks are neighbouring channels, 16 bytes of them.
+template <typename IO, typename F> wtconv_status norm_variant(int C, bool vec, F f) {
+  if (vec) return norm_shape<sizeof(IO) == 2 ? 8 : 4>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::true_type(), t); });
+  return norm_shape<8>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::false_type(), t); });
 }
 
 // Calls f with the I/O type (and the type of the residual).
@@ -420,11 +422,13 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
     a.lengths = lengths;
     a.strip = causal_forward_strip(desc);
     a.strips = (int)ceil_div(T, a.strip);
-    constexpr int V = 4;  // more would fill the registers with taps and windows
-    const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(y, V, e, B, T) && wide(state, V, e) &&
-                     wide(state_out, V, e);
+    // channels of a thread: more than four would fill the registers with taps and windows
+    auto fits = [&](int V) {
+      return C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(y, V, e, B, T) && wide(state, V, e) && wide(state_out, V, e);
+    };
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return vec ? causal_forward<IO, V>(a, desc->k, st) : causal_forward<IO, 1>(a, desc->k, st);
+    if (fits(4)) return causal_forward<IO, 4>(a, desc->k, st);
+    return fits(2) ? causal_forward<IO, 2>(a, desc->k, st) : causal_forward<IO, 1>(a, desc->k, st);
   });
 }
 
@@ -459,11 +463,16 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
     a.part = static_cast<float*>(ws);
     a.strip = causal_grad_strip(desc);
     a.strips = (int)causal_grad_strips(desc);
-    constexpr int V = sizeof(IO) == 2 ? 4 : 2;  // taps, windows, sums and loads ahead fill the registers
-    const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(dy, V, e, B, T) &&
-                     wide(dx, V, e, B, T) && wide(state, V, e) && wide(dstate_out, V, e) && wide(dstate, V, e);
+    // taps, windows, sums and loads ahead of four 16-bit or two 32-bit channels fill the registers
+    auto fits = [&](int V) {
+      return C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, T) && wide(dy, V, e, B, T) && wide(dx, V, e, B, T) &&
+             wide(state, V, e) && wide(dstate_out, V, e) && wide(dstate, V, e);
+    };
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return vec ? causal_backward<IO, V>(a, desc->k, dw, dbias, st) : causal_backward<IO, 1>(a, desc->k, dw, dbias, st);
+    if constexpr (sizeof(IO) == 2) {
+      if (fits(4)) return causal_backward<IO, 4>(a, desc->k, dw, dbias, st);
+    }
+    return fits(2) ? causal_backward<IO, 2>(a, desc->k, dw, dbias, st) : causal_backward<IO, 1>(a, desc->k, dw, dbias, st);
   });
 }
 
@@ -617,13 +626,13 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
       const bool vec = C % V == 0 && wide(x, V, sizeof(IO), B, T) && wide(gate, V, sizeof(IO), B, T) &&
                        wide(y, V, sizeof(IO), B, T) && wide(res, V, sizeof(RES), B, T) &&
                        wide(res_out, V, sizeof(RES), B, T);
-      return norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
+      return norm_variant<IO>(C, vec, [&](auto v, auto nv, auto wide, int threads) {
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         const int blocks = norm_blocks(desc, threads, v.value * nv.value <= 8 ? NORM_THREADS : 512);
         if (v.value * nv.value <= 8 && threads <= 256)
-          norm_forward_kernel<IO, RES, v.value, nv.value, 256><<<blocks, threads, 0, st>>>(a);
+          norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 256><<<blocks, threads, 0, st>>>(a);
         else
-          norm_forward_kernel<IO, RES, v.value, nv.value, 512><<<blocks, threads, 0, st>>>(a);
+          norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 512><<<blocks, threads, 0, st>>>(a);
         return launched();
       });
     });
@@ -670,9 +679,9 @@ wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_ro
                        wide(dres_out, V, re, B, T) && wide(dres, V, re, B, T);
       cudaStream_t st = static_cast<cudaStream_t>(stream);
       int blocks = 0;
-      TRY((norm_variant<IO, RES>(C, vec, [&](auto v, auto nv, int threads) {
+      TRY((norm_variant<IO>(C, vec, [&](auto v, auto nv, auto wide, int threads) {
         blocks = norm_blocks(desc, threads, NORM_GRAD_THREADS);
-        norm_backward_kernel<IO, RES, v.value, nv.value><<<blocks, threads, 0, st>>>(a);
+        norm_backward_kernel<IO, RES, v.value, nv.value, wide.value><<<blocks, threads, 0, st>>>(a);
         return launched();
       })));
       if (!dw && !dscale && !dw_res) return WTCONV_OK;

@@ -57,6 +57,8 @@ template <typename IO, int V> struct Raw {
         *reinterpret_cast<uint4*>(&r[k]) = __ldg(reinterpret_cast<const uint4*>(p + k * W));
       else if constexpr (sizeof(Pack<IO, W>) == 8)
         *reinterpret_cast<uint2*>(&r[k]) = __ldg(reinterpret_cast<const uint2*>(p + k * W));
+      else if constexpr (W == 2)
+        *reinterpret_cast<unsigned*>(&r[k]) = __ldg(reinterpret_cast<const unsigned*>(p + k * W));
       else
         r[k].v[0] = __ldg(p + k * W);
     }

@@ -1,7 +1,7 @@
 // Norms before and after a block with its gate and residual scale.
 //
 // A block of threads holds one row at a time in registers, NV chunks of V
-// neighbouring channels a thread: each input is read once and each output
+// channels a thread: each input is read once and each output
 // written once.  A block goes through its rows with the parameters of its
 // channels, and for the gradients the sums over the rows, in registers; where
 // these fit (8 values a thread) the next row's inputs are on their way while a
@@ -70,66 +70,90 @@ template <typename IO> __device__ __forceinline__ IO* row_at(const Rows<IO>& r, 
   return r.p + b * r.sb + (long long)t * (int)r.st;
 }
 
+// The channels of a thread's chunk i: V neighbours, which are all there or none,
+// or (WIDE = false, for rows that begin at odd addresses) V channels a block
+// apart, so that each access of a warp is still one piece of the row.
+template <int V, bool WIDE> struct Cols {
+  static __device__ __forceinline__ int at(int i, int k) {
+    return WIDE ? (i * blockDim.x + threadIdx.x) * V + k : (i * V + k) * blockDim.x + threadIdx.x;
+  }
+  static __device__ __forceinline__ bool none(int i, int C) { return at(i, 0) >= C; }
+  template <typename IO> static __device__ __forceinline__ void store(IO* row, int i, int C, const float (&f)[V]) {
+    if constexpr (WIDE) {
+      store_pack<IO, V>(row + at(i, 0), f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (at(i, k) < C) row[at(i, k)] = from_f<IO>(f[k]);
+    }
+  }
+  template <typename IO> static __device__ __forceinline__ void load(const IO* row, int i, int C, Raw<IO, V>& r) {
+    if constexpr (WIDE) {
+      r.load(row + at(i, 0));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) r.r[k / r.W].v[k % r.W] = at(i, k) < C ? __ldg(row + at(i, k)) : from_f<IO>(0.f);
+    }
+  }
+};
+
 // The fp32 parameters of a thread's channels: kept in registers, or loaded
 // where they are used.
 // (one where there is none; the product of two)
-template <int V, int NV, bool KEEP> struct Params {
+template <int V, int NV, bool WIDE, bool KEEP> struct Params {
   const float *p, *p2;
   Vals<V> kept[KEEP ? NV : 1];
-  __device__ __forceinline__ Vals<V> load(int c) const {
+  int C;
+  __device__ __forceinline__ Vals<V> load(int i) const {
     float f[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = (p ? __ldg(p + c + k) : 1.f) * (p2 ? __ldg(p2 + c + k) : 1.f);
+    for (int k = 0; k < V; ++k) {
+      const int c = Cols<V, WIDE>::at(i, k);
+      f[k] = c < C ? (p ? __ldg(p + c) : 1.f) * (p2 ? __ldg(p2 + c) : 1.f) : 0.f;
+    }
     Vals<V> v;
     v.set(f);
     return v;
   }
-  __device__ __forceinline__ Params(const float* p, const float* p2, int C) : p(p), p2(p2) {
+  __device__ __forceinline__ Params(const float* p, const float* p2, int C) : p(p), p2(p2), C(C) {
     if constexpr (KEEP) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < C)
-          kept[i] = load(c);
-        else
-          kept[i].zero();
-      }
+      for (int i = 0; i < NV; ++i) kept[i] = load(i);
     }
   }
-  __device__ __forceinline__ Vals<V> get(int i, int c) const {
+  __device__ __forceinline__ Vals<V> get(int i) const {
     if constexpr (KEEP)
       return kept[i];
     else
-      return load(c);
+      return load(i);
   }
 };
 
 // One row of an input as it lies in memory.
-template <typename IO, int V, int NV> struct RowIn {
+template <typename IO, int V, int NV, bool WIDE> struct RowIn {
   Raw<IO, V> r[NV];
   __device__ __forceinline__ void load(const Rows<IO>& in, int b, int t, int C) {
     if (!in.p) return;
     const IO* p = row_at(in, b, t);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c < C) r[i].load(p + c);
+      if (!Cols<V, WIDE>::none(i, C)) Cols<V, WIDE>::load(p, i, C, r[i]);
     }
   }
 };
 
 // NT: the most threads of a block.  Rows of 8 values a thread run at 64
 // registers, which fills an SM with 1024 threads.
-template <typename IO, typename RES, int V, int NV, int NT>
+template <typename IO, typename RES, int V, int NV, bool WIDE, int NT>
 __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_forward_kernel(NormArgs<IO, RES> a) {
   constexpr bool AHEAD = V * NV <= 8;
   __shared__ __align__(16) float sums[2][2][1][NORM_WARPS];
   for (int i = threadIdx.x; i < 4 * NORM_WARPS; i += blockDim.x) sums[0][0][0][i] = 0.f;
   __syncthreads();
   const float per = 1.f / a.C;
-  const Params<V, NV, AHEAD> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);  // res_out = res + sw u n1
-  RowIn<IO, V, NV> x, gate;
-  RowIn<RES, V, NV> res;
+  const Params<V, NV, WIDE, AHEAD> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);  // res_out = res + sw u n1
+  RowIn<IO, V, NV, WIDE> x, gate;
+  RowIn<RES, V, NV, WIDE> res;
   NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
   auto load = [&] {
     const int b = then.b, t = then.t;
@@ -148,10 +172,9 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
     if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
 #pragma unroll
         for (int k = 0; k < V; ++k) u[i][k] = r[i][k] = 0.f;
-        if (c >= a.C) continue;
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
         x.r[i].floats(u[i]);
         if (a.gate.p) {
           float g[V];
@@ -165,9 +188,10 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
     if (AHEAD) load(), then.next();
     if (!live) {
       const float zero[V] = {};
-      for (int c = threadIdx.x * V; c < a.C; c += blockDim.x * V) {
-        if (a.y.p) store_pack<IO, V>(row_at(a.y, b, t) + c, zero);
-        if (a.res_out.p) store_pack<RES, V>(row_at(a.res_out, b, t) + c, zero);
+      for (int i = 0; i < NV; ++i) {
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
+        if (a.y.p) Cols<V, WIDE>::store(row_at(a.y, b, t), i, a.C, zero);
+        if (a.res_out.p) Cols<V, WIDE>::store(row_at(a.res_out, b, t), i, a.C, zero);
       }
       continue;
     }
@@ -184,16 +208,15 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
     float q[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c >= a.C) continue;
+      if (Cols<V, WIDE>::none(i, a.C)) continue;
       float f[V];
-      sw.get(i, c).get(f);
+      sw.get(i).get(f);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         u[i][k] = fmaf(f[k], u[i][k] * n1, r[i][k]);
         q[0] = fmaf(u[i][k], u[i][k], q[0]);
       }
-      if (a.res.p) store_pack<RES, V>(row_at(a.res_out, b, t) + c, u[i]);
+      if (a.res.p) Cols<V, WIDE>::store(row_at(a.res_out, b, t), i, a.C, u[i]);
     }
     if (a.w_res) {
       block_sum(q, sums[turn][1]);
@@ -202,15 +225,14 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
     if (!a.y.p) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c >= a.C) continue;
+      if (Cols<V, WIDE>::none(i, a.C)) continue;
       float f[V];
       if (a.w_res) {
-        w_res.get(i, c).get(f);
+        w_res.get(i).get(f);
 #pragma unroll
         for (int k = 0; k < V; ++k) u[i][k] *= n2 * f[k];
       }
-      store_pack<IO, V>(row_at(a.y, b, t) + c, u[i]);
+      Cols<V, WIDE>::store(row_at(a.y, b, t), i, a.C, u[i]);
     }
   }
 }
@@ -222,7 +244,7 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
 //   dx = du silu(gate)   dgate = du x silu'(gate)
 // Without res, dr is dy.  dscale and dw share the sum over the rows, and scale
 // and w are only needed as their product until the end.
-template <typename IO, typename RES, int V, int NV>
+template <typename IO, typename RES, int V, int NV, bool WIDE>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES> a) {
   constexpr bool AHEAD = V * NV <= 8, KEEP = AHEAD;
   constexpr int P = Vals<V>::P;
@@ -230,12 +252,12 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
   for (int i = threadIdx.x; i < 2 * NORM_WARPS; i += blockDim.x) s1[0][0][i] = s2[0][0][i] = s2[1][0][i] = s3[0][0][i] = 0.f;
   __syncthreads();
   const float per = 1.f / a.C;
-  const Params<V, NV, KEEP> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);
+  const Params<V, NV, WIDE, KEEP> sw(a.w, a.scale, a.C), w_res(a.w_res, nullptr, a.C);
   Vals<V> as[NV], ar[NV];  // S and dw_res
 #pragma unroll
   for (int i = 0; i < NV; ++i) as[i].zero(), ar[i].zero();
-  RowIn<IO, V, NV> x, gate, dy;
-  RowIn<RES, V, NV> res, dres;
+  RowIn<IO, V, NV, WIDE> x, gate, dy;
+  RowIn<RES, V, NV, WIDE> res, dres;
   NormRows now(a.B, a.T), then = now;  // the row to work on, and to load
   auto load = [&] {
     const int b = then.b, t = then.t;
@@ -271,7 +293,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         u[i].zero(), act[i].zero(), xd[i].zero(), r[i].zero(), q[i].zero(), g[i].zero();
-        if ((i * blockDim.x + threadIdx.x) * V >= a.C) continue;
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
         u[i] = vals(x.r[i]);
         if (a.gate.p) {
           act[i] = vals(gate.r[i]);
@@ -293,10 +315,11 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
     if (AHEAD) load(), then.next();
     if (!live) {
       const float zero[V] = {};
-      for (int c = threadIdx.x * V; c < a.C; c += blockDim.x * V) {
-        store_pack<IO, V>(row_at(a.dx, b, t) + c, zero);
-        if (a.gate.p) store_pack<IO, V>(row_at(a.dgate, b, t) + c, zero);
-        if (a.res.p) store_pack<RES, V>(row_at(a.dres, b, t) + c, zero);
+      for (int i = 0; i < NV; ++i) {
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
+        Cols<V, WIDE>::store(row_at(a.dx, b, t), i, a.C, zero);
+        if (a.gate.p) Cols<V, WIDE>::store(row_at(a.dgate, b, t), i, a.C, zero);
+        if (a.res.p) Cols<V, WIDE>::store(row_at(a.dres, b, t), i, a.C, zero);
       }
       continue;
     }
@@ -315,9 +338,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
       f32x2 rr = 0, rt = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) continue;
-        const Vals<V> f = sw.get(i, c), fr = w_res.get(i, c);
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
+        const Vals<V> f = sw.get(i), fr = w_res.get(i);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           r[i].p[k] = fma2(f.p[k], u[i].p[k], r[i].p[k]);
@@ -334,9 +356,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.C) continue;
-        const Vals<V> fr = w_res.get(i, c);
+        if (Cols<V, WIDE>::none(i, a.C)) continue;
+        const Vals<V> fr = w_res.get(i);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           const f32x2 qn = mul2(q[i].p[k], twice(n2));  // zero without w_res, and m too
@@ -345,15 +366,14 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
         }
         float f[V];
         q[i].get(f);
-        store_pack<RES, V>(row_at(a.dres, b, t) + c, f);
+        Cols<V, WIDE>::store(row_at(a.dres, b, t), i, a.C, f);
       }
     }
     f32x2 uq = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c >= a.C) continue;
-      const Vals<V> f = sw.get(i, c);
+      if (Cols<V, WIDE>::none(i, a.C)) continue;
+      const Vals<V> f = sw.get(i);
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         as[i].p[k] = fma2(q[i].p[k], u[i].p[k], as[i].p[k]);
@@ -372,8 +392,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c >= a.C) continue;
+      if (Cols<V, WIDE>::none(i, a.C)) continue;
       float f[V];
       if (a.gate.p) {
 #pragma unroll
@@ -382,24 +401,25 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
           q[i].p[k] = mul2(q[i].p[k], act[i].p[k]);
         }
         xd[i].get(f);
-        store_pack<IO, V>(row_at(a.dgate, b, t) + c, f);
+        Cols<V, WIDE>::store(row_at(a.dgate, b, t), i, a.C, f);
       }
       q[i].get(f);
-      store_pack<IO, V>(row_at(a.dx, b, t) + c, f);
+      Cols<V, WIDE>::store(row_at(a.dx, b, t), i, a.C, f);
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c >= a.C) continue;
-    float* p = a.part + (long long)blockIdx.x * 3 * a.C + c;
+    if (Cols<V, WIDE>::none(i, a.C)) continue;
+    float* p = a.part + (long long)blockIdx.x * 3 * a.C;
     float f1[V], f2[V];
     as[i].get(f1), ar[i].get(f2);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      p[k] = f1[k] * (a.scale ? __ldg(a.scale + c + k) : 1.f);
-      p[a.C + k] = f1[k] * (a.w ? __ldg(a.w + c + k) : 1.f);
-      p[2 * a.C + k] = f2[k];
+      const int c = Cols<V, WIDE>::at(i, k);
+      if (c >= a.C) continue;
+      p[c] = f1[k] * (a.scale ? __ldg(a.scale + c) : 1.f);
+      p[a.C + c] = f1[k] * (a.w ? __ldg(a.w + c) : 1.f);
+      p[2 * a.C + c] = f2[k];
     }
   }
 }
