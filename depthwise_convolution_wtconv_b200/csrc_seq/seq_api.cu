@@ -161,20 +161,59 @@ wtconv_status check_scan(const wtconv_scan_desc* d) {
   return d->N > WTCONV_SCAN_MAX_N ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
 }
 
-struct ScanWs {  // floats into the workspace
-  size_t ckpt, part_b, part_c, part_a, part_d, part_bias, end;
-};
 int scan_blocks(const wtconv_scan_desc* d) { return (int)ceil_div(d->C / d->G, 32); }
-ScanWs scan_backward_ws(const wtconv_scan_desc* d) {
+
+// Chunks of a row: as many as it takes to give every SM SCAN_FILL blocks, of
+// at least SCAN_CHUNK tiles.  A cut row pays the recurrence twice, so rows are
+// cut only where whole ones leave half of that idle.
+constexpr int SCAN_FILL = 4, SCAN_CHUNK = 4;
+void scan_plan(const wtconv_scan_desc* d, int* chunks, int* chunk_tiles) {
+  const long long rows = (long long)d->B * scan_blocks(d) * d->G, tiles = ceil_div(d->T, SCAN_T);
+  long long n = 1;
+  if (rows * 2 <= SMS * SCAN_FILL) n = std::max(1ll, std::min(SMS * SCAN_FILL / rows, tiles / SCAN_CHUNK));
+  *chunk_tiles = (int)ceil_div(tiles, n);
+  *chunks = (int)ceil_div(tiles, *chunk_tiles);
+}
+
+// A group's channels and states as the kernels read them: rounded up to 16
+// bytes and to four, by copies where that is more than there are.
+int scan_group(const wtconv_scan_desc* d) {
+  const int e = (int)(16 / elt(d->io));
+  return (int)ceil_div(d->C / d->G, e) * e;
+}
+int scan_states(const wtconv_scan_desc* d) { return (d->N + 3) / 4 * 4; }
+
+struct ScanWs {  // bytes into the workspace, each part on 16
+  size_t ends, sums, grad_ends, pads, ckpt, part_b, part_c, part_a, part_d, part_bias, end;
+};
+ScanWs scan_ws(const wtconv_scan_desc* d, bool backward) {
   ScanWs w;
-  const size_t bc = (size_t)scan_blocks(d) * d->G * d->B * d->T * d->N, tiles = ceil_div(d->T, SCAN_T);
-  w.ckpt = 0;
-  w.part_b = w.ckpt + tiles * (SCAN_T / SCAN_S) * d->B * d->N * d->C;
-  w.part_c = w.part_b + bc;
-  w.part_a = w.part_c + bc;
-  w.part_d = w.part_a + (size_t)d->B * d->C * d->N;
-  w.part_bias = w.part_d + (size_t)d->B * d->C;
-  w.end = w.part_bias + (size_t)d->B * d->C;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += rup16(n);
+    return r;
+  };
+  int chunks, per;
+  scan_plan(d, &chunks, &per);
+  const size_t tokens = (size_t)d->B * d->T, bc = (size_t)d->B * d->C, cut = chunks > 1 ? chunks : 0;
+  w.ends = take(cut * bc * d->N * 4);
+  w.sums = take(cut * bc * 4);
+  w.grad_ends = take(backward ? cut * bc * d->N * 4 : 0);
+  w.pads = at;
+  if (scan_group(d) != d->C / d->G)
+    for (int k = 0; k < (backward ? 4 : 3); ++k) take(tokens * d->G * scan_group(d) * elt(d->io));
+  if (scan_states(d) != d->N)
+    for (int k = 0; k < 2; ++k) take(tokens * d->G * scan_states(d) * elt(d->io));
+  if (backward) {
+    w.ckpt = take(ceil_div(d->T, SCAN_T) * (SCAN_T / SCAN_S) * bc * d->N * 4);
+    w.part_b = take(scan_blocks(d) * tokens * d->G * d->N * 4);
+    w.part_c = take(scan_blocks(d) * tokens * d->G * d->N * 4);
+    w.part_a = take(chunks * bc * d->N * 4);
+    w.part_d = take(chunks * bc * 4);
+    w.part_bias = take(chunks * bc * 4);
+  }
+  w.end = at;
   return w;
 }
 
@@ -199,10 +238,8 @@ ScanArgs<IO> scan_args(const wtconv_scan_desc* d, const wtconv_rows* x, const wt
   p.softplus = d->softplus;
   p.blocks = scan_blocks(d);
   p.tiles = (int)ceil_div(d->T, SCAN_T);
-  const size_t e = sizeof(IO);
-  const int V = 16 / sizeof(IO);
-  p.wide_x = (d->C / d->G) % V == 0 && wide(x, V, e, d->B, d->T) && wide(dt, V, e, d->B, d->T) && wide(z, V, e, d->B, d->T);
-  p.wide_bc = d->N % V == 0 && wide(b, V, e, d->B, d->T) && wide(c, V, e, d->B, d->T);
+  p.group = d->C / d->G;
+  p.states = d->N;
   return p;
 }
 
@@ -228,24 +265,6 @@ template <typename K> wtconv_status allow_smem(K kernel, size_t bytes) {
              : WTCONV_ERR_CUDA;
 }
 
-// Chunks of a row: as many as it takes to give every SM SCAN_FILL blocks, of
-// at least SCAN_CHUNK tiles.  A cut row pays the recurrence twice, so rows are
-// cut only where whole ones leave half of that idle.
-constexpr int SCAN_FILL = 4, SCAN_CHUNK = 4;
-void scan_plan(const wtconv_scan_desc* d, int* chunks, int* chunk_tiles) {
-  const long long rows = (long long)d->B * scan_blocks(d) * d->G, tiles = ceil_div(d->T, SCAN_T);
-  long long n = 1;
-  if (rows * 2 <= SMS * SCAN_FILL) n = std::max(1ll, std::min(SMS * SCAN_FILL / rows, tiles / SCAN_CHUNK));
-  *chunk_tiles = (int)ceil_div(tiles, n);
-  *chunks = (int)ceil_div(tiles, *chunk_tiles);
-}
-// Floats of the chunks' ends and sums (0: rows are not cut).
-size_t scan_chunk_floats(const wtconv_scan_desc* d) {
-  int chunks, per;
-  scan_plan(d, &chunks, &per);
-  return chunks == 1 ? 0 : (size_t)chunks * d->B * d->C * (d->N + 1);
-}
-
 // Calls f with the warps of a block: SCAN_J states each.
 template <typename F> wtconv_status with_warps(int N, F f) {
   if (N <= SCAN_J) return f(Int<1>());
@@ -260,23 +279,55 @@ template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>&
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
   return with_warps(p.N, [&](auto W) {
-    const size_t smem = ScanSmem<IO>(nullptr, p.N, W.value).end - (char*)nullptr;
+    const size_t smem = ScanSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
     TRY((allow_smem(scan_forward_kernel<IO, MODE, W.value>, smem)));
     scan_forward_kernel<IO, MODE, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
   });
 }
 
-// The chunks' ends where rows are cut, then y or the states before each tile.
-template <typename IO, int MODE>
-wtconv_status run_scan_forward(const wtconv_scan_desc* d, ScanArgs<IO>& p, float* chunk_ws, cudaStream_t st) {
+// The plan of a pass, the copies that it needs, and the chunks' ends where
+// rows are cut.
+template <typename IO>
+wtconv_status scan_prepare(const wtconv_scan_desc* d, ScanArgs<IO>& p, bool backward, char* ws, cudaStream_t st) {
+  const ScanWs w = scan_ws(d, backward);
   scan_plan(d, &p.chunks, &p.chunk_tiles);
-  if (p.chunks > 1) {
-    p.ends = chunk_ws;
-    p.sums = chunk_ws + (size_t)p.chunks * p.B * p.C * p.N;
-    TRY((run_scan_pass<IO, SCAN_ENDS>(p, st)));
+  p.ends = reinterpret_cast<float*>(ws + w.ends);
+  p.sums = reinterpret_cast<float*>(ws + w.sums);
+  p.grad_ends = reinterpret_cast<float*>(ws + w.grad_ends);
+  ScanPad<IO> pad = {};
+  pad.lengths = p.lengths;
+  pad.B = p.B, pad.T = p.T, pad.G = p.G;
+  int n = 0;
+  char* at = ws + w.pads;
+  auto copy = [&](Rows<IO>& r, int from, int to) {
+    if (!r.p) return;
+    pad.in[n] = r, pad.from[n] = from, pad.to[n] = to;
+    pad.out[n] = reinterpret_cast<IO*>(at);
+    const long long row = (long long)p.G * to;
+    r = Rows<IO>{pad.out[n], row * p.T, row};
+    at += rup16((size_t)p.B * p.T * row * sizeof(IO));
+    ++n;
+  };
+  if (scan_group(d) != p.group) {
+    copy(p.x, p.group, scan_group(d)), copy(p.dt, p.group, scan_group(d)), copy(p.z, p.group, scan_group(d));
+    if (backward) copy(p.dy, p.group, scan_group(d));
+    p.group = scan_group(d);
   }
-  return run_scan_pass<IO, MODE>(p, st);
+  if (scan_states(d) != p.states) {
+    copy(p.b, p.states, scan_states(d)), copy(p.c, p.states, scan_states(d));
+    p.states = scan_states(d);
+  }
+  if (n) {
+    scan_pad_kernel<IO><<<dim3(SMS * 4, n), 256, 0, st>>>(pad);
+    TRY(launched());
+  }
+  auto fits = [&](const Rows<IO>& r, size_t bytes) {
+    return aligned(r.p, bytes) && (p.B == 1 || r.sb * sizeof(IO) % bytes == 0) && (p.T == 1 || r.st * sizeof(IO) % bytes == 0);
+  };
+  p.wide_x = fits(p.x, 16) && fits(p.dt, 16) && fits(p.z, 16) && (!backward || fits(p.dy, 16));
+  p.wide_bc = fits(p.b, 4 * sizeof(IO)) && fits(p.c, 4 * sizeof(IO));
+  return p.chunks > 1 ? run_scan_pass<IO, SCAN_ENDS>(p, st) : WTCONV_OK;
 }
 
 // Sums of db or dc: output i = ((g * B + b) * T + t) * N + n
@@ -294,20 +345,20 @@ template <typename IO> struct ScanRowSums {
 
 template <typename IO>
 wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, const wtconv_rows* db, const wtconv_rows* dc,
-                                float* da, float* dd, float* ddt_bias, float* ws, cudaStream_t st) {
-  const ScanWs w = scan_backward_ws(d);
-  p.ckpt = ws + w.ckpt;
-  p.part_b = ws + w.part_b;
-  p.part_c = ws + w.part_c;
-  p.part_a = ws + w.part_a;
-  p.part_d = ws + w.part_d;
-  p.part_bias = ws + w.part_bias;
-  TRY((run_scan_forward<IO, SCAN_CKPT>(d, p, ws + w.end, st)));
-  p.chunks = 1;
-  p.chunk_tiles = p.tiles;
-  const long long blocks = (long long)p.B * p.blocks * p.G;
+                                float* da, float* dd, float* ddt_bias, char* ws, cudaStream_t st) {
+  TRY(scan_prepare<IO>(d, p, true, ws, st));
+  const ScanWs w = scan_ws(d, true);
+  p.ckpt = reinterpret_cast<float*>(ws + w.ckpt);
+  p.part_b = reinterpret_cast<float*>(ws + w.part_b);
+  p.part_c = reinterpret_cast<float*>(ws + w.part_c);
+  p.part_a = reinterpret_cast<float*>(ws + w.part_a);
+  p.part_d = reinterpret_cast<float*>(ws + w.part_d);
+  p.part_bias = reinterpret_cast<float*>(ws + w.part_bias);
+  TRY((run_scan_pass<IO, SCAN_CKPT>(p, st)));
+  if (p.chunks > 1) TRY((run_scan_pass<IO, SCAN_GRAD_ENDS>(p, st)));
+  const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks, parts = (long long)p.chunks * p.B;
   TRY(with_warps(p.N, [&](auto W) {
-    const size_t smem = ScanGradSmem<IO>(nullptr, p.N, W.value).end - (char*)nullptr;
+    const size_t smem = ScanGradSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
     TRY((allow_smem(scan_backward_kernel<IO, W.value>, smem)));
     scan_backward_kernel<IO, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
@@ -316,9 +367,9 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
   launch_sum(p.part_b, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(db), p.B, p.T, p.N}, st);
   launch_sum(p.part_c, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(dc), p.B, p.T, p.N}, st);
   const long long cn = (long long)p.C * p.N;
-  launch_sum(p.part_a, p.B, cn, cn, SumFloats{da}, st);
-  if (dd) launch_sum(p.part_d, p.B, p.C, p.C, SumFloats{dd}, st);
-  if (ddt_bias) launch_sum(p.part_bias, p.B, p.C, p.C, SumFloats{ddt_bias}, st);
+  launch_sum(p.part_a, parts, cn, cn, SumFloats{da}, st);
+  if (dd) launch_sum(p.part_d, parts, p.C, p.C, SumFloats{dd}, st);
+  if (ddt_bias) launch_sum(p.part_bias, parts, p.C, p.C, SumFloats{ddt_bias}, st);
   return launched();
 }
 
@@ -503,7 +554,7 @@ wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_ro
 
 size_t wtconv_scan_workspace_size(const wtconv_scan_desc* desc, int backward) {
   if (check_scan(desc) != WTCONV_OK || (backward != 0 && backward != 1)) return 0;
-  return rup16(((backward ? scan_backward_ws(desc).end : 0) + scan_chunk_floats(desc)) * sizeof(float));
+  return scan_ws(desc, backward).end;
 }
 
 wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_rows* x, const wtconv_rows* dt,
@@ -524,7 +575,9 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
     p.state = state;
     p.state_out = state_out;
     p.lengths = lengths;
-    return run_scan_forward<IO, SCAN_Y>(desc, p, static_cast<float*>(ws), static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    TRY(scan_prepare<IO>(desc, p, false, static_cast<char*>(ws), st));
+    return run_scan_pass<IO, SCAN_Y>(p, st);
   });
 }
 
@@ -568,7 +621,7 @@ wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_ro
     p.dstate_out = dstate_out;
     p.dstate = dstate;
     p.lengths = lengths;
-    return run_scan_backward<IO>(desc, p, db, dc, da, dd, ddt_bias, static_cast<float*>(ws),
+    return run_scan_backward<IO>(desc, p, db, dc, da, dd, ddt_bias, static_cast<char*>(ws),
                                  static_cast<cudaStream_t>(stream));
   });
 }

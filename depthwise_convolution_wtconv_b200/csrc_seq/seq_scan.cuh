@@ -16,6 +16,7 @@
 // tiles, each chunk a block: a first pass finds each chunk's state from a zero
 // start and its sum of delta (the decay over the chunk is exp(a sum delta)),
 // and every chunk of the second pass joins those before it into its start.
+// The gradients do the same from the other end.
 #pragma once
 
 #include "seq_common.cuh"
@@ -38,11 +39,13 @@ template <typename IO> struct ScanArgs {
   const int* lengths;
   float* ends;               // [chunks][B][N][C] states after each chunk from a zero start
   float* sums;               // [chunks][B][C] sums of delta over each chunk
+  float* grad_ends;          // [chunks][B][N][C] their gradients before each chunk, from zero behind it
   float* ckpt;               // [B][tiles * SCAN_T / SCAN_S][N][C] states before every SCAN_S tokens
   float *part_b, *part_c;    // [C blocks][B][T][N]
-  float *part_a;             // [B][C][N]
-  float *part_d, *part_bias; // [B][C]
+  float *part_a;             // [chunks][B][C][N]
+  float *part_d, *part_bias; // [chunks][B][C]
   int B, T, C, N, G, softplus;
+  int group, states;  // channels and states of a group as x, dt, z, dy and b, c hold them (rounded up if copied)
   int blocks;       // blocks of 32 channels in a group
   int tiles;        // of a row
   int chunks;       // of a row
@@ -57,6 +60,11 @@ template <typename IO> struct ScanArgs {
 // multiply-add that forms them.
 constexpr float EXP_BIAS = 1.8e-8f * 1.4426950408889634f;
 
+template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src, bool valid) {  // zeros where not valid
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  const int n = valid ? BYTES : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {  // zeros where not valid
   const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
   const int n = valid ? 16 : 0;
@@ -68,8 +76,8 @@ template <int PENDING> __device__ __forceinline__ void copies_wait() {
 }
 
 // A lane's share of the copies of one input, tile by tile, 16 bytes at a time
-// where the rows suit that: pointers that only move on.  Tokens behind the
-// length become zeros.  `wide` decides between the two forms below.
+// where the rows begin at such addresses (`wide`), one by one where not:
+// pointers that only move on.  Tokens behind the length become zeros.
 template <typename IO> struct RowCopy {  // [SCAN_T][32 channels]
   static constexpr int E = 16 / sizeof(IO), PER = 32 / E, ROWS = 32 / PER;  // elements, chunks a row, rows a pass
   const IO* p;
@@ -88,15 +96,18 @@ template <typename IO> struct RowCopy {  // [SCAN_T][32 channels]
 #pragma unroll
       for (int k = 0; k < SCAN_T; k += ROWS) copy16(s + at + k * 32, p + (long long)k * st, k < left);
     } else {
-#pragma unroll 4
-      for (int k = 0; k < SCAN_T; ++k) s[at + k * 32] = k < left ? p[(long long)k * st] : from_f<IO>(0.f);
+      IO v[SCAN_T];
+#pragma unroll
+      for (int k = 0; k < SCAN_T; ++k) v[k] = k < left ? __ldg(p + (long long)k * st) : from_f<IO>(0.f);
+#pragma unroll
+      for (int k = 0; k < SCAN_T; ++k) s[at + k * 32] = v[k];
     }
     left -= dir * SCAN_T;
     p += (long long)(dir * SCAN_T) * st;
   }
 };
-// The tiles of b or c, [SCAN_T][N states]: the chunks of a row of N, and the
-// lane's first token and state; `step` tokens a pass (0: not a whole number).
+// The tiles of b or c, [SCAN_T][states]: the chunks of a row (four states, or
+// one), and the lane's first token and state; `step` tokens a pass (0: not a whole number).
 struct StateLanes {
   int per, t, k, step;
   __device__ __forceinline__ StateLanes(int N, int e) {
@@ -112,14 +123,14 @@ __device__ __forceinline__ void copy_states(const StateLanes& l, const Rows<IO>&
   const int st = (int)r.st;
   auto one = [&](int t, int k) {
     if (wide)
-      copy16(s + t * N + k, p + (long long)t * st + k, t < left);
+      copy_async<4 * sizeof(IO)>(s + t * N + k, p + (long long)t * st + k, t < left);
     else
       s[t * N + k] = t < left ? p[(long long)t * st + k] : from_f<IO>(0.f);
   };
   if (l.step) {
     for (int u = l.t; u < SCAN_T; u += l.step) one(u, l.k);
   } else {
-    const int e = wide ? 16 / sizeof(IO) : 1;
+    const int e = wide ? 4 : 1;
     for (int i = threadIdx.x & 31; i < SCAN_T * l.per; i += 32) one(i / l.per, i % l.per * e);
   }
 }
@@ -135,10 +146,10 @@ template <typename IO, int W, int R> struct TileCopies {
   int left;      // tokens from there on
   __device__ __forceinline__ TileCopies(const ScanArgs<IO>& p, const Rows<IO> (&in)[R], int row, int t0, int stop, long long col,
                                         int g)
-      : lanes(p.N, p.wide_bc ? 16 / sizeof(IO) : 1), left(stop - t0) {
+      : lanes(p.states, p.wide_bc ? 4 : 1), left(stop - t0) {
     const int warp = threadIdx.x >> 5;
-    bc = (W == 1 || warp == R % W ? p.b : p.c).at(row, t0) + (long long)g * p.N;
-    other = p.c.at(row, t0) + (long long)g * p.N;
+    bc = (W == 1 || warp == R % W ? p.b : p.c).at(row, t0) + (long long)g * p.states;
+    other = p.c.at(row, t0) + (long long)g * p.states;
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
       Rows<IO> r = in[0];
@@ -147,7 +158,7 @@ template <typename IO, int W, int R> struct TileCopies {
       for (int k = i * W; k < R && k < (i + 1) * W; ++k)
         if (k == i * W + warp) r = in[k], to[i] = k;
       if (!r.p) to[i] = -1;
-      if (to[i] >= 0) rows[i] = RowCopy<IO>(r, row, t0, stop, col, p.C, p.wide_x);
+      if (to[i] >= 0) rows[i] = RowCopy<IO>(r, row, t0, stop, col, (long long)p.G * p.group, p.wide_x);
     }
   }
   __device__ __forceinline__ void tile(const ScanArgs<IO>& p, int slot, int slots, int dir, IO* x, IO* to_b, IO* to_c) {
@@ -156,35 +167,37 @@ template <typename IO, int W, int R> struct TileCopies {
     for (int i = 0; i < MINE; ++i)
       if (to[i] >= 0) rows[i].tile(p.wide_x, dir, x + (to[i] * slots + slot) * (SCAN_T * 32));
     if (W == 1) {  // both
-      copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.N, to_b + slot * SCAN_T * p.N);
-      if (to_c) copy_states<IO>(lanes, p.c, other, left, p.wide_bc, p.N, to_c + slot * SCAN_T * p.N);
+      if (to_b) copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.states, to_b + slot * SCAN_T * p.states);
+      if (to_c) copy_states<IO>(lanes, p.c, other, left, p.wide_bc, p.states, to_c + slot * SCAN_T * p.states);
       other += (long long)(dir * SCAN_T) * (int)p.c.st;
-    } else if (warp == R % W) {
-      copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.N, to_b + slot * SCAN_T * p.N);
+    } else if (to_b && warp == R % W) {
+      copy_states<IO>(lanes, p.b, bc, left, p.wide_bc, p.states, to_b + slot * SCAN_T * p.states);
     } else if (to_c && warp == (R + 1) % W) {
-      copy_states<IO>(lanes, p.c, bc, left, p.wide_bc, p.N, to_c + slot * SCAN_T * p.N);
+      copy_states<IO>(lanes, p.c, bc, left, p.wide_bc, p.states, to_c + slot * SCAN_T * p.states);
     }
     bc += (long long)(dir * SCAN_T) * (int)(W == 1 || warp == R % W ? p.b : p.c).st;
     left -= dir * SCAN_T;
   }
 };
 
-// b and c of a tile, [t][n], as fp32 [n][t]: a thread per token and two states.
-template <typename IO, int W, bool BOTH>
+// b, c or both of a tile, [t][n], as fp32 [n][t]: a thread per token and two states.
+template <typename IO, int W, bool HAS_B, bool HAS_C>
 __device__ __forceinline__ void transpose_tiles(const IO* b, const IO* c, int N, float* tb, float* tc) {
   const int t = threadIdx.x % SCAN_T;
   if (N & 1) {
     for (int n = threadIdx.x / SCAN_T; n < N; n += W * 32 / SCAN_T) {
-      tb[n * SCAN_LD + t] = to_f<IO>(b[t * N + n]);
-      if (BOTH) tc[n * SCAN_LD + t] = to_f<IO>(c[t * N + n]);
+      if (HAS_B) tb[n * SCAN_LD + t] = to_f<IO>(b[t * N + n]);
+      if (HAS_C) tc[n * SCAN_LD + t] = to_f<IO>(c[t * N + n]);
     }
     return;
   }
   for (int n = threadIdx.x / SCAN_T * 2; n < N; n += W * 64 / SCAN_T) {
-    const Pack<IO, 2> u = *reinterpret_cast<const Pack<IO, 2>*>(b + t * N + n);
-    tb[n * SCAN_LD + t] = to_f<IO>(u.v[0]);
-    tb[(n + 1) * SCAN_LD + t] = to_f<IO>(u.v[1]);
-    if (BOTH) {
+    if (HAS_B) {
+      const Pack<IO, 2> u = *reinterpret_cast<const Pack<IO, 2>*>(b + t * N + n);
+      tb[n * SCAN_LD + t] = to_f<IO>(u.v[0]);
+      tb[(n + 1) * SCAN_LD + t] = to_f<IO>(u.v[1]);
+    }
+    if (HAS_C) {
       const Pack<IO, 2> v = *reinterpret_cast<const Pack<IO, 2>*>(c + t * N + n);
       tc[n * SCAN_LD + t] = to_f<IO>(v.v[0]);
       tc[(n + 1) * SCAN_LD + t] = to_f<IO>(v.v[1]);
@@ -192,10 +205,38 @@ __device__ __forceinline__ void transpose_tiles(const IO* b, const IO* c, int N,
   }
 }
 
+// Copies of inputs whose rows cannot be read 16 bytes at a time, because a
+// group's channels (or states) are no multiple of that: [B][T][G][to], the
+// group rounded up and filled with zeros.  A thread makes E elements; block
+// row y is input y.
+template <typename IO> struct ScanPad {
+  Rows<IO> in[6];
+  IO* out[6];
+  int from[6], to[6];  // channels or states of a group
+  const int* lengths;
+  int B, T, G;
+};
+template <typename IO> __global__ void __launch_bounds__(256) scan_pad_kernel(const ScanPad<IO> p) {
+  constexpr int E = 4;
+  const int k = blockIdx.y, from = p.from[k], to = p.to[k], per = p.G * to / E;
+  const long long all = (long long)p.B * p.T * per;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const long long row = i / per;
+    const int col = (int)(i - row * per) * E, g = col / to, o = col - g * to;
+    const int b = (int)(row / p.T), t = (int)(row - (long long)b * p.T);
+    if (t >= row_length(p.lengths, b, p.T)) continue;
+    const IO* const r = p.in[k].at(b, t) + (long long)g * from;
+    Pack<IO, E> v;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v.v[e] = o + e < from ? __ldg(r + o + e) : from_f<IO>(0.f);
+    *reinterpret_cast<Pack<IO, E>*>(p.out[k] + row * per * E + col) = v;
+  }
+}
+
 // What a block works on.
 struct ScanPlace {
   int b, g, c, chunk, len, tile0, tile1;  // tile1: behind the last tile with tokens
-  long long col;                          // of the block's first channel
+  long long col;                          // of the block's first channel, in x, dt, z and dy
   bool on;                                // whether the lane has a channel
 };
 template <typename IO> __device__ __forceinline__ ScanPlace scan_place(const ScanArgs<IO>& p) {
@@ -209,8 +250,8 @@ template <typename IO> __device__ __forceinline__ ScanPlace scan_place(const Sca
   w.g = blk / p.blocks;
   const int off = (blk % p.blocks) * 32;
   w.on = off + lane < per;
-  w.col = (long long)w.g * per + off;
-  w.c = (int)w.col + (w.on ? lane : 0);
+  w.col = (long long)w.g * p.group + off;
+  w.c = w.g * per + off + (w.on ? lane : 0);
   w.len = row_length(p.lengths, w.b, p.T);
   w.tile0 = w.chunk * p.chunk_tiles;
   w.tile1 = min(w.tile0 + p.chunk_tiles, (w.len + SCAN_T - 1) / SCAN_T);
@@ -234,7 +275,20 @@ template <typename IO> __device__ __forceinline__ float scan_start(const ScanArg
   return h;
 }
 
-enum { SCAN_Y, SCAN_ENDS, SCAN_CKPT };  // y; the chunks' ends and sums; the states before every SCAN_S tokens
+// e behind the block's chunk: that of the row's last state joined with the chunks behind.
+template <typename IO> __device__ __forceinline__ float scan_grad_start(const ScanArgs<IO>& p, const ScanPlace& w, int n, float a) {
+  float e = p.dstate_out ? p.dstate_out[((long long)w.b * p.C + w.c) * p.N + n] : 0.f;
+  for (int k = p.chunks - 1; k > w.chunk; --k) {
+    const long long r = (long long)k * p.B + w.b;
+    e = fmaf(exp2_approx(p.sums[r * p.C + w.c] * a), e, p.grad_ends[(r * p.N + n) * p.C + w.c]);
+  }
+  return e;
+}
+
+// What a pass is for: y; the chunks' ends and sums; the states before every
+// SCAN_S tokens; the gradients before each chunk (tokens last to first, with
+// c dp in the place of b delta x).
+enum { SCAN_Y, SCAN_ENDS, SCAN_CKPT, SCAN_GRAD_ENDS };
 
 // A thread's tokens of a tile in A and C are R = SCAN_T / W neighbours, kept as
 // [t / 4][lane][t % 4]: four tokens of a lane are one 16-byte access.
@@ -323,10 +377,13 @@ template <typename IO, int MODE, int W>
 __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_kernel(const ScanArgs<IO> p) {
   extern __shared__ __align__(16) char scan_smem[];
   constexpr int J = SCAN_J, NP = J * W, R = SCAN_T / W;
-  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
-  const ScanSmem<IO> s(scan_smem, N, W);
+  constexpr bool BACK = MODE == SCAN_GRAD_ENDS;
+  constexpr int DIR = BACK ? -1 : 1;
+  const int N = p.N, NS = p.states, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
+  const ScanSmem<IO> s(scan_smem, NS, W);
   const ScanPlace w = scan_place(p);
-  const bool gated = MODE == SCAN_Y && p.z.p;
+  const bool gated = (MODE == SCAN_Y || BACK) && p.z.p;
+  if (BACK && w.chunk == 0) return;  // nothing comes before
   if (MODE == SCAN_ENDS && w.chunk == p.chunks - 1) {  // nothing comes after
     for (int n = warp; w.on && n < N; n += W)
       p.ends[(((long long)w.chunk * p.B + w.b) * N + n) * p.C + w.c] = scan_first(p, w, n);
@@ -334,12 +391,13 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
   }
   const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f;
   const float dskip = MODE == SCAN_Y && p.d ? __ldg(p.d + w.c) : 0.f;
-  const int first = w.tile0 * SCAN_T, count = max(0, w.tile1 - w.tile0);
-  const Rows<IO> none = {nullptr, 0, 0}, in[3] = {p.x, p.dt, gated ? p.z : none};
+  const int count = max(0, w.tile1 - w.tile0);
+  const int first = max(0, BACK ? (w.tile1 - 1) * SCAN_T : w.tile0 * SCAN_T);  // token of the first tile to do
+  const Rows<IO> none = {nullptr, 0, 0}, in[3] = {BACK ? p.dy : p.x, p.dt, gated ? p.z : none};
   TileCopies<IO, W, 3> copies(p, in, w.b, first, w.len, w.col, w.g);
-  // the phases count tiles from the block's first; copies and C go in order
+  // the phases count tiles from the block's first to do; copies and C go in order
   auto copy = [&](int k) {
-    if (k < count) copies.tile(p, k % SCAN_SLOTS, SCAN_SLOTS, 1, s.x, s.b, MODE == SCAN_Y ? s.c : nullptr);
+    if (k < count) copies.tile(p, k % SCAN_SLOTS, SCAN_SLOTS, DIR, s.x, BACK ? nullptr : s.b, MODE == SCAN_Y || BACK ? s.c : nullptr);
     copies_commit();
   };
   float sum = 0.f;                               // of this thread's delta
@@ -356,20 +414,26 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
 #pragma unroll
       for (int i = 0; i < R; ++i) de[i] = softplus(de[i]);
     }
-    const int left = mine - (int)k * SCAN_T;
+    const int left = mine - DIR * (int)k * SCAN_T;
     if (left < R) {
 #pragma unroll
       for (int i = 0; i < R; ++i) de[i] = i < left ? de[i] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (MODE == SCAN_ENDS) sum += de[i];
-      dx[i] = de[i] * to_f<IO>(x[i * 32]);
+      if (MODE == SCAN_ENDS || BACK) sum += de[i];
+      dx[i] = to_f<IO>(x[i * 32]);
+      if (!BACK) {
+        dx[i] *= de[i];
+      } else if (gated) {
+        const float z = to_f<IO>(s.z[(slot * SCAN_T + warp * R + i) * 32 + lane]);
+        dx[i] *= z * sigmoid(z);
+      }
     }
     put_tokens<R>(s.de + buf * SCAN_T * 32 + own, de);
     put_tokens<R>(s.dx + buf * SCAN_T * 32 + own, dx);
-    transpose_tiles<IO, W, MODE == SCAN_Y>(s.b + slot * SCAN_T * N, s.c + slot * SCAN_T * N, N, s.tb + buf * (NP * SCAN_LD),
-                                           s.tc + buf * (NP * SCAN_LD));
+    transpose_tiles<IO, W, !BACK, MODE == SCAN_Y || BACK>(s.b + slot * SCAN_T * NS, s.c + slot * SCAN_T * NS, NS,
+                                                          s.tb + buf * (NP * SCAN_LD), s.tc + buf * (NP * SCAN_LD));
   };
   f32x2 a2[J];  // a log2(e), twice
   float h[J];
@@ -380,6 +444,23 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
     const ulonglong2* dx = reinterpret_cast<const ulonglong2*>(s.dx) + buf * SCAN_T * 8 + lane;
     const float* tb = s.tb + (buf * NP + n0) * SCAN_LD;
     const float* tc = s.tc + (buf * NP + n0) * SCAN_LD;
+    if constexpr (BACK) {
+#pragma unroll
+      for (int q = SCAN_T / 4 - 1; q >= 0; --q) {
+        const ulonglong2 d = de[q * 32], u = dx[q * 32];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const ulonglong2 cq = *reinterpret_cast<const ulonglong2*>(tc + j * SCAN_LD + 4 * q);
+          float e0, e1, e2, e3, c0, c1, c2, c3;
+          unpair(fma2(d.x, a2[j], bias2), e0, e1), unpair(fma2(d.y, a2[j], bias2), e2, e3);
+          unpair(mul2(u.x, cq.x), c0, c1), unpair(mul2(u.y, cq.y), c2, c3);
+          h[j] = exp2_approx(e3) * (h[j] + c3);
+          h[j] = exp2_approx(e2) * (h[j] + c2);
+          h[j] = exp2_approx(e1) * (h[j] + c1);
+          h[j] = exp2_approx(e0) * (h[j] + c0);
+        }
+      }
+    } else {
 #pragma unroll
     for (int q = 0; q < SCAN_T / 4; ++q) {
       if (MODE == SCAN_CKPT && q % (SCAN_S / 4) == 0 && w.on) {
@@ -409,6 +490,7 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
       if (MODE == SCAN_Y)
         reinterpret_cast<ulonglong2*>(s.y)[((buf * W + warp) * (SCAN_T / 4) + q) * 32 + lane] = make_ulonglong2(y01, y23);
     }
+    }
   };
   IO* out = MODE == SCAN_Y ? p.y.at(w.b, first + warp * R) + w.c : nullptr;
   auto phase_c = [&](unsigned k) {
@@ -435,15 +517,15 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
 
   copy(0);
   copy(1);
-  for (int i = threadIdx.x; i < 2 * (NP - N) * SCAN_LD; i += W * 32) {  // states that are not there
-    const int k = i / ((NP - N) * SCAN_LD), r = i % ((NP - N) * SCAN_LD) + (k * NP + N) * SCAN_LD;
+  for (int i = threadIdx.x; i < 2 * (NP - NS) * SCAN_LD; i += W * 32) {  // states that are not there
+    const int k = i / ((NP - NS) * SCAN_LD), r = i % ((NP - NS) * SCAN_LD) + (k * NP + NS) * SCAN_LD;
     s.tb[r] = s.tc[r] = 0.f;
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const float a = n0 + j < N ? __ldg(p.a + (long long)w.c * N + n0 + j) * LOG2E : 0.f;
     a2[j] = twice(a);
-    h[j] = MODE == SCAN_ENDS || n0 + j >= N ? 0.f : scan_start(p, w, n0 + j, a);
+    h[j] = MODE == SCAN_ENDS || BACK || n0 + j >= N ? 0.f : scan_start(p, w, n0 + j, a);
   }
   copies_wait<0>();
   __syncthreads();
@@ -470,19 +552,19 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
       for (int j = 0; j < J; ++j)
         if (n0 + j < N) p.state_out[((long long)w.b * p.C + w.c) * N + n0 + j] = h[j];
   }
-  if constexpr (MODE == SCAN_ENDS) {
+  if constexpr (MODE == SCAN_ENDS || BACK) {
     const long long r = (long long)w.chunk * p.B + w.b;
     s.y[warp * 32 + lane] = sum;
     __syncthreads();
     if (!w.on) return;
-    if (warp == 0) {
+    if (warp == 0 && (!BACK || w.chunk == p.chunks - 1)) {  // the last chunk has no other pass that needs its sum
 #pragma unroll
       for (int k = 1; k < W; ++k) sum += s.y[k * 32 + lane];
       p.sums[r * p.C + w.c] = sum;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (n0 + j < N) p.ends[(r * N + n0 + j) * p.C + w.c] = h[j];
+      if (n0 + j < N) (BACK ? p.grad_ends : p.ends)[(r * N + n0 + j) * p.C + w.c] = h[j];
   }
 }
 
@@ -544,8 +626,8 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
   extern __shared__ __align__(16) char scan_smem[];
   constexpr int J = SCAN_J, NP = J * W, R = SCAN_T / W;
   static_assert(J == 4 && SCAN_S == 8 && SCAN_T == 2 * SCAN_S, "the exchanges below are written for these");
-  const int N = p.N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
-  const ScanGradSmem<IO> s(scan_smem, N, W);
+  const int N = p.N, NS = p.states, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = warp * J;
+  const ScanGradSmem<IO> s(scan_smem, NS, W);
   const ScanPlace w = scan_place(p);
   const bool gated = p.z.p;
   const float bias = p.dt_bias ? __ldg(p.dt_bias + w.c) : 0.f, dskip = p.d ? __ldg(p.d + w.c) : 0.f;
@@ -588,7 +670,7 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
     put_tokens<R>(s.de + own, de);
     put_tokens<R>(s.dx + own, dx);
     put_tokens<R>(s.dp + own, dp);
-    transpose_tiles<IO, W, true>(s.b + k % SCAN_GSLOTS * SCAN_T * N, s.c + k % SCAN_GSLOTS * SCAN_T * N, N, s.tb, s.tc);
+    transpose_tiles<IO, W, true, true>(s.b + k % SCAN_GSLOTS * SCAN_T * NS, s.c + k % SCAN_GSLOTS * SCAN_T * NS, NS, s.tb, s.tc);
   };
 
   // the states of this lane's registers
@@ -600,8 +682,9 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
   for (int j = 0; j < J; ++j) {
     nj[j] = n0 + (j ^ (lane & 3));
     const bool there = nj[j] < N;
-    a2[j] = twice(there ? __ldg(p.a + (long long)w.c * N + nj[j]) * LOG2E : 0.f);
-    e[j] = there && w.on && p.dstate_out ? p.dstate_out[((long long)w.b * p.C + w.c) * N + nj[j]] : 0.f;
+    const float a = there ? __ldg(p.a + (long long)w.c * N + nj[j]) * LOG2E : 0.f;
+    a2[j] = twice(a);
+    e[j] = there && w.on ? scan_grad_start(p, w, nj[j], a) : 0.f;
     da2[j] = 0;
   }
   auto fetch = [&](int token) {
@@ -743,7 +826,7 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
 
   copy(0);
   copy(1);
-  for (int i = threadIdx.x; i < (NP - N) * SCAN_LD; i += W * 32) s.tb[N * SCAN_LD + i] = s.tc[N * SCAN_LD + i] = 0.f;
+  for (int i = threadIdx.x; i < (NP - NS) * SCAN_LD; i += W * 32) s.tb[NS * SCAN_LD + i] = s.tc[NS * SCAN_LD + i] = 0.f;
   fetch(last + SCAN_T - SCAN_S);
   copies_wait<0>();
   __syncthreads();
@@ -773,11 +856,10 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     if (!w.on || nj[j] >= N) continue;
-    const long long i = ((long long)w.b * p.C + w.c) * N + nj[j];
     float a, b;
     unpair(da2[j], a, b);
-    p.part_a[i] = a + b;
-    if (p.dstate) p.dstate[i] = e[j];
+    p.part_a[(((long long)w.chunk * p.B + w.b) * p.C + w.c) * N + nj[j]] = a + b;
+    if (p.dstate && w.chunk == 0) p.dstate[((long long)w.b * p.C + w.c) * N + nj[j]] = e[j];
   }
   s.y[warp * 32 + lane] = acc_d;
   s.y[(W + warp) * 32 + lane] = acc_bias;
@@ -785,8 +867,8 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
   if (warp == 0 && w.on) {
 #pragma unroll
     for (int k = 1; k < W; ++k) acc_d += s.y[k * 32 + lane], acc_bias += s.y[(W + k) * 32 + lane];
-    p.part_d[(long long)w.b * p.C + w.c] = acc_d;
-    p.part_bias[(long long)w.b * p.C + w.c] = acc_bias;
+    p.part_d[((long long)w.chunk * p.B + w.b) * p.C + w.c] = acc_d;
+    p.part_bias[((long long)w.chunk * p.B + w.b) * p.C + w.c] = acc_bias;
   }
 }
 
