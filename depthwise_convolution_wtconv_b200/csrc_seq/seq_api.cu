@@ -330,22 +330,13 @@ wtconv_status scan_prepare(const wtconv_scan_desc* d, ScanArgs<IO>& p, bool back
   return p.chunks > 1 ? run_scan_pass<IO, SCAN_ENDS>(p, st) : WTCONV_OK;
 }
 
-// Sums of db or dc: output i = ((g * B + b) * T + t) * N + n
-template <typename IO> struct ScanRowSums {
-  Rows<IO> out;
-  int B, T, N;
-  __device__ __forceinline__ void put(long long i, float v) const {
-    const int n = (int)(i % N);
-    long long r = i / N;
-    const long long t = r % T;
-    r /= T;
-    out.at((int)(r % B), t)[r / B * N + n] = from_f<IO>(v);
-  }
-};
-
 template <typename IO>
 wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, const wtconv_rows* db, const wtconv_rows* dc,
                                 float* da, float* dd, float* ddt_bias, char* ws, cudaStream_t st) {
+  // the sums take the most blocks
+  if (!grid_ok(2 * ceil_div((long long)p.G * p.B * p.T * p.N, 32) + (long long)p.C * (p.N + 2)) ||
+      !grid_ok((long long)p.B * p.blocks * p.G * ceil_div(p.tiles, SCAN_CHUNK)))
+    return WTCONV_ERR_UNSUPPORTED;
   TRY(scan_prepare<IO>(d, p, true, ws, st));
   const ScanWs w = scan_ws(d, true);
   p.ckpt = reinterpret_cast<float*>(ws + w.ckpt);
@@ -363,13 +354,24 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
     scan_backward_kernel<IO, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
   }));
+  ScanSums<IO> sums = {};
+  sums.db = rows_of<IO>(db), sums.dc = rows_of<IO>(dc);
+  sums.B = p.B, sums.T = p.T, sums.N = p.N;
+  long long first = 0;
+  int k = 0;
+  auto add = [&](const float* part, long long P, long long n, float* to) {
+    sums.part[k] = part, sums.P[k] = P, sums.n[k] = n, sums.to[k] = to;
+    sums.first[k++] = first;
+    first += to || k <= 2 ? ceil_div(n, 32) : 0;
+  };
   const long long bc = (long long)p.G * p.B * p.T * p.N;
-  launch_sum(p.part_b, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(db), p.B, p.T, p.N}, st);
-  launch_sum(p.part_c, p.blocks, bc, bc, ScanRowSums<IO>{rows_of<IO>(dc), p.B, p.T, p.N}, st);
-  const long long cn = (long long)p.C * p.N;
-  launch_sum(p.part_a, parts, cn, cn, SumFloats{da}, st);
-  if (dd) launch_sum(p.part_d, parts, p.C, p.C, SumFloats{dd}, st);
-  if (ddt_bias) launch_sum(p.part_bias, parts, p.C, p.C, SumFloats{ddt_bias}, st);
+  add(p.part_b, p.blocks, bc, nullptr);
+  add(p.part_c, p.blocks, bc, nullptr);
+  add(p.part_a, parts, (long long)p.C * p.N, da);
+  add(p.part_d, parts, p.C, dd);
+  add(p.part_bias, parts, p.C, ddt_bias);
+  sums.first[k] = first;
+  scan_sums_kernel<IO><<<(unsigned)first, 256, 0, st>>>(sums);
   return launched();
 }
 

@@ -189,27 +189,16 @@ __device__ __forceinline__ float softplus(float v) {
 
 // out[i] = sum over p of part[p * stride + i] in a fixed order: a block holds
 // 32 outputs x 8 slices of p, each summed in order, the slices joined in order.
-struct SumFloats {
-  float* out;
-  __device__ __forceinline__ void put(long long i, float v) const { out[i] = v; }
-};
-template <typename IO> struct SumRows {  // i = (b * T + t) * W + w
-  Rows<IO> out;
-  int T, W;
-  __device__ __forceinline__ void put(long long i, float v) const {
-    const long long r = i / W;
-    out.at((int)(r / T), r % T)[i % W] = from_f<IO>(v);
-  }
-};
-
 template <typename Target>
-__global__ void __launch_bounds__(256) sum_partials(const float* __restrict__ part, long long P, long long stride, long long n, Target target) {
+__device__ __forceinline__ void sum_block(const float* __restrict__ part, long long P, long long stride, long long n, long long block,
+                                          const Target& target) {
   __shared__ float s[8][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const long long i = (long long)blockIdx.x * 32 + x;
+  const long long i = block * 32 + x;
   float v = 0.f;
   if (i < n) {
     const long long per = (P + 7) / 8, p1 = (y + 1) * per < P ? (y + 1) * per : P;
+#pragma unroll 8
     for (long long p = y * per; p < p1; ++p) v += __ldg(part + p * stride + i);
   }
   s[y][x] = v;
@@ -219,6 +208,11 @@ __global__ void __launch_bounds__(256) sum_partials(const float* __restrict__ pa
     for (int k = 1; k < 8; ++k) v += s[k][x];
     target.put(i, v);
   }
+}
+
+template <typename Target>
+__global__ void __launch_bounds__(256) sum_partials(const float* __restrict__ part, long long P, long long stride, long long n, Target target) {
+  sum_block(part, P, stride, n, blockIdx.x, target);
 }
 
 template <typename Target>

@@ -872,6 +872,45 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 16 / W) scan_backward_ke
   }
 }
 
+// The sums over blocks, batch rows and chunks of all gradients, in one launch:
+// db and dc (type of the I/O), da, dd and ddt_bias, each in its share of the
+// blocks.
+template <typename IO> struct ScanSums {
+  const float* part[5];
+  long long P[5], n[5], first[6];  // parts and values of a sum; its first block
+  Rows<IO> db, dc;
+  float* to[5];
+  int B, T, N;
+};
+template <typename IO> struct ScanSumRows {
+  Rows<IO> out;
+  int B, T, N;
+  __device__ __forceinline__ void put(long long i, float v) const {
+    const int n = (int)(i % N);  // i = ((g * B + b) * T + t) * N + n
+    long long r = i / N;
+    const long long t = r % T;
+    r /= T;
+    out.at((int)(r % B), t)[r / B * N + n] = from_f<IO>(v);
+  }
+};
+struct ScanSumFloats {
+  float* out;
+  __device__ __forceinline__ void put(long long i, float v) const { out[i] = v; }
+};
+template <typename IO> __global__ void __launch_bounds__(256) scan_sums_kernel(const ScanSums<IO> p) {
+  const long long x = blockIdx.x;
+  if (x < p.first[1])
+    sum_block(p.part[0], p.P[0], p.n[0], p.n[0], x, ScanSumRows<IO>{p.db, p.B, p.T, p.N});
+  else if (x < p.first[2])
+    sum_block(p.part[1], p.P[1], p.n[1], p.n[1], x - p.first[1], ScanSumRows<IO>{p.dc, p.B, p.T, p.N});
+  else if (x < p.first[3])
+    sum_block(p.part[2], p.P[2], p.n[2], p.n[2], x - p.first[2], ScanSumFloats{p.to[2]});
+  else if (x < p.first[4])
+    sum_block(p.part[3], p.P[3], p.n[3], p.n[3], x - p.first[3], ScanSumFloats{p.to[3]});
+  else
+    sum_block(p.part[4], p.P[4], p.n[4], p.n[4], x - p.first[4], ScanSumFloats{p.to[4]});
+}
+
 // One token of every row: four threads share a channel's states and join their
 // sums over the four.  With VEC, four states at a time: the state, 8 bytes a
 // state of traffic where everything else is less than one, goes in 16-byte

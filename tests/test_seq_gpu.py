@@ -421,3 +421,145 @@ def test_scan_state_updated_in_place(cuda_ok, T):
         s = d["state"].clone()
         y2, _ = wt.scan_forward(*args, state=s, state_out=s, lengths=lengths)
         assert torch.equal(y, y2) and torch.equal(s, state)
+
+
+# -------------------------------------------------------- a block of all three
+def _block(g, C, E, N, R):
+    """Parameters of a gated state space block of C channels, E inside, on the CPU."""
+    r = lambda *s: torch.randn(*s, generator=g)
+    step = torch.exp(torch.rand(E, generator=g) * 4.6 - 6.9)
+    return dict(w_in=r(2 * E, C) / C ** 0.5, conv=r(E, 4) / 2, conv_b=0.1 * r(E), w_x=r(R + 2 * N, E) / E ** 0.5,
+                w_dt=r(E, R) / R ** 0.5, dt_bias=step + torch.log(-torch.expm1(-step)),
+                a=-torch.arange(1, N + 1, dtype=torch.float32).repeat(E, 1), d=1 + 0.1 * r(E), w=1 + 0.1 * r(E),
+                w_out=r(C, E) / E ** 0.5, scale=0.5 + 0.1 * r(C), w_res=1 + 0.1 * r(C))
+
+
+def _split(p, proj, N, R):
+    return proj[..., :R] @ p["w_dt"].t(), proj[..., R: R + N], proj[..., R + N:]
+
+
+def _prompt(p, u, res, N, R, lengths=None, states=(None, None)):
+    """The block over a prompt: its outputs and every tensor its gradients need."""
+    E = p["d"].shape[0]
+    xz = u @ p["w_in"].t()
+    x, z = xz[..., :E], xz[..., E:]
+    xc, s1 = wt.causal_forward(x, p["conv"], p["conv_b"], state=states[0], lengths=lengths)
+    dt, b, c = _split(p, xc @ p["w_x"].t(), N, R)
+    y, s2 = wt.scan_forward(xc, dt, p["a"], b, c, p["d"], None, p["dt_bias"], state=states[1], lengths=lengths)
+    v, _ = wt.norm_forward(y, p["w"], gate=z, lengths=lengths)
+    o = v @ p["w_out"].t()
+    out, res2 = wt.norm_forward(o, None, res=res, scale=p["scale"], w_res=p["w_res"], lengths=lengths)
+    return out, res2, (s1, s2), (x, z, xc, dt, b, c, y, v, o)
+
+
+def _reference_block(p, u, res, N, R):
+    """The same block in float64 torch, token by token, differentiable."""
+    E = p["d"].shape[0]
+    xz = u @ p["w_in"].t()
+    x, z = xz[..., :E], xz[..., E:]
+    pad = torch.nn.functional.pad(x, (0, 0, 3, 0))
+    xc = torch.nn.functional.silu((pad.unfold(1, 4, 1) * p["conv"]).sum(-1) + p["conv_b"])
+    dt, b, c = _split(p, xc @ p["w_x"].t(), N, R)
+    step = torch.nn.functional.softplus(dt + p["dt_bias"])
+    h, ys = torch.zeros(u.shape[0], E, N, dtype=u.dtype), []
+    for t in range(u.shape[1]):
+        h = torch.exp(step[:, t, :, None] * p["a"]) * h + (step[:, t] * xc[:, t])[..., None] * b[:, t, None]
+        ys.append((h * c[:, t, None]).sum(-1) + p["d"] * xc[:, t])
+    g = torch.stack(ys, 1) * torch.nn.functional.silu(z)
+    v = g * torch.rsqrt(g.square().mean(-1, keepdim=True) + 1e-6) * p["w"]
+    r = res + p["scale"] * (v @ p["w_out"].t())
+    return r * torch.rsqrt(r.square().mean(-1, keepdim=True) + 1e-6) * p["w_res"], r
+
+
+def test_block_for_training(cuda_ok):
+    """norm, convolution, scan and gate together in fp32: outputs and the gradients of the inputs and of every parameter
+    against float64 differentiation.  Tolerance 2e-4 of each tensor's norm: about 3 T + E + C = 300 operations of 2^-21 in
+    a row, each at most its share of the norm."""
+    torch.backends.cuda.matmul.allow_tf32 = False
+    B, T, C, E, N, R = 2, 40, 48, 96, 16, 6
+    g = torch.Generator().manual_seed(11)
+    p = _block(g, C, E, N, R)
+    u, res = torch.randn(B, T, C, generator=g), torch.randn(B, T, C, generator=g)
+    dout, dres = torch.randn(B, T, C, generator=g), torch.randn(B, T, C, generator=g)
+    q = {k: v.double().requires_grad_() for k, v in p.items()}
+    u64, r64 = u.double().requires_grad_(), res.double().requires_grad_()
+    want, want_res = _reference_block(q, u64, r64, N, R)
+    ((want * dout).sum() + (want_res * dres).sum()).backward()
+
+    P = {k: v.cuda() for k, v in p.items()}
+    ud, rd = u.cuda(), res.cuda()
+    out, res2, _, (x, z, xc, dt, b, c, y, v, o) = _prompt(P, ud, rd, N, R)
+    got = {}
+    n2 = wt.norm_backward(o, dout.cuda(), res=rd, scale=P["scale"], w_res=P["w_res"], dres=dres.cuda())
+    got.update(scale=n2["dscale"], w_res=n2["dw_res"], res=n2["dres"])
+    do = n2["dx"]
+    got["w_out"] = torch.einsum("btc,bte->ce", do, v)
+    n1 = wt.norm_backward(y, do @ P["w_out"], P["w"], gate=z)
+    got["w"] = n1["dw"]
+    s = wt.scan_backward(xc, dt, P["a"], b, c, n1["dx"], P["d"], None, P["dt_bias"])
+    got.update(a=s["da"], d=s["dd"], dt_bias=s["ddt_bias"])
+    proj = xc @ P["w_x"].t()
+    dproj = torch.cat([s["ddt"] @ P["w_dt"], s["db"], s["dc"]], -1)
+    got["w_dt"] = torch.einsum("bte,btr->er", s["ddt"], proj[..., :R])
+    got["w_x"] = torch.einsum("btr,bte->re", dproj, xc)
+    dx, gc = wt.causal_backward(x, s["dx"] + dproj @ P["w_x"], P["conv"], P["conv_b"])
+    got.update(conv=gc["dw"], conv_b=gc["db"])
+    dxz = torch.cat([dx, n1["dgate"]], -1)
+    got["w_in"] = torch.einsum("bte,btc->ec", dxz, ud)
+    got["u"] = dxz @ P["w_in"]
+    ref = {**{k: t.grad for k, t in q.items()}, "u": u64.grad, "res": r64.grad}
+    pairs = [("out", out, want), ("res", res2, want_res)] + [("d" + k, got[k], ref[k]) for k in ref]
+    for name, a, w in pairs:
+        err = (a.double().cpu() - w.detach()).norm() / w.detach().norm()
+        assert err < 2e-4, (name, float(err))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_block_for_serving(cuda_ok, io):
+    """A padded batch of prompts, then single tokens from the states it left, in a captured graph that is replayed: the same
+    as one longer prompt.  bf16: each of the five activations behind an output is rounded by 2^-8, 2^-5 in all."""
+    torch.backends.cuda.matmul.allow_tf32 = False
+    B, T, more, C, E, N, R = 3, 33, 6, 32, 64, 16, 4
+    g = torch.Generator().manual_seed(12)
+    dt_ = sc.DT[io]
+    P = {k: v.cuda() if k in ("conv", "conv_b", "dt_bias", "a", "d", "w", "scale", "w_res") else v.to(dt_).cuda()
+         for k, v in _block(g, C, E, N, R).items()}
+    n = [33, 1, 20]
+    lengths = torch.tensor(n, dtype=torch.int32, device="cuda")
+    u, res = (torch.randn(B, T + more, C, generator=g).to(dt_).cuda() for _ in range(2))
+    # row i of the batch: its first n[i] tokens as the prompt (NaN behind), the next ones singly
+    pu, pr = u[:, :T].clone(), res[:, :T].clone()
+    for i, k in enumerate(n):
+        pu[i, k:], pr[i, k:] = float("nan"), float("nan")
+    _, _, (s1, s2), _ = _prompt(P, pu, pr, N, R, lengths)
+    tok_u, tok_r = torch.empty(B, C, dtype=dt_, device="cuda"), torch.empty(B, C, dtype=dt_, device="cuda")
+
+    def token():
+        xz = tok_u @ P["w_in"].t()
+        xc = wt.causal_step(xz[:, :E], s1, P["conv"], P["conv_b"])
+        dt, b, c = _split(P, xc @ P["w_x"].t(), N, R)
+        y = wt.scan_step(xc, dt, s2, P["a"], b, c, P["d"], None, P["dt_bias"])
+        v, _ = wt.norm_forward(y, P["w"], gate=xz[:, E:])
+        return wt.norm_forward(v @ P["w_out"].t(), None, res=tok_r, scale=P["scale"], w_res=P["w_res"])
+    tok_u.zero_(), tok_r.zero_()
+    keep = s1.clone(), s2.clone()
+    token()  # the library's first use, and the matrix products', outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, res2 = token()
+    s1.copy_(keep[0]), s2.copy_(keep[1])
+    got = []
+    for j in range(more):
+        tok_u.copy_(torch.stack([u[i, n[i] + j] for i in range(B)]))
+        tok_r.copy_(torch.stack([res[i, n[i] + j] for i in range(B)]))
+        graph.replay()
+        got.append((out.clone(), res2.clone()))
+    whole = torch.tensor([k + more for k in n], dtype=torch.int32, device="cuda")
+    want, want_res, states, _ = _prompt(P, u, res, N, R, whole)
+    tol = 1e-4 if io == "f32" else 2.0 ** -5
+    rel = lambda a, b: float((a.double() - b.double()).norm() / b.double().norm())
+    for i in range(B):
+        assert rel(torch.stack([o[i] for o, _ in got]), want[i, n[i]: n[i] + more]) < tol
+        assert rel(torch.stack([r[i] for _, r in got]), want_res[i, n[i]: n[i] + more]) < tol
+    assert rel(s1, states[0]) < tol and rel(s2, states[1]) < tol
