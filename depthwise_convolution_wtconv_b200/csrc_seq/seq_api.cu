@@ -16,6 +16,7 @@ namespace {
 
 constexpr long long MAX_ELEMENTS = 1ll << 56;  // byte offsets stay within 64 bits
 constexpr long long MAX_TOKEN_STRIDE = INT_MAX;  // kernels hold it in 32 bits
+constexpr int MAX_TOKENS = 1 << 30;  // of a row: token counts and tiles stay within 32 bits
 constexpr int SMS = 148;
 
 size_t elt(wtconv_dtype t) { return t == WTCONV_F32 ? 4 : 2; }
@@ -73,7 +74,7 @@ bool grid_ok(long long blocks) { return blocks <= INT_MAX; }
 
 // ------------------------------------------------------ causal convolution
 wtconv_status check_causal(const wtconv_causal_desc* d) {
-  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || d->k <= 0 || !dtype_ok(d->io)) return WTCONV_ERR_ARG;
+  if (!d || d->B <= 0 || d->T <= 0 || d->T > MAX_TOKENS || d->C <= 0 || d->k <= 0 || !dtype_ok(d->io)) return WTCONV_ERR_ARG;
   if ((long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
   return d->k > WTCONV_CAUSAL_MAX_K ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
 }
@@ -155,7 +156,7 @@ wtconv_status causal_step(const CausalArgs<IO>& a, int k, const int* active, cud
 
 // -------------------------------------------------------------------- scan
 wtconv_status check_scan(const wtconv_scan_desc* d) {
-  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || d->N <= 0 || d->G <= 0 || d->C % d->G || !dtype_ok(d->io))
+  if (!d || d->B <= 0 || d->T <= 0 || d->T > MAX_TOKENS || d->C <= 0 || d->N <= 0 || d->G <= 0 || d->C % d->G || !dtype_ok(d->io))
     return WTCONV_ERR_ARG;
   if ((long long)d->B * d->T > MAX_ELEMENTS / d->C / 64) return WTCONV_ERR_ARG;
   return d->N > WTCONV_SCAN_MAX_N ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
@@ -166,11 +167,12 @@ int scan_blocks(const wtconv_scan_desc* d) { return (int)ceil_div(d->C / d->G, 3
 // Chunks of a row: as many as it takes to give every SM SCAN_FILL blocks, of
 // at least SCAN_CHUNK tiles.  A cut row pays the recurrence twice, so rows are
 // cut only where whole ones leave half of that idle.
-constexpr int SCAN_FILL = 4, SCAN_CHUNK = 4;
+// At most SCAN_CHUNKS, since a chunk joins all those before it one by one.
+constexpr int SCAN_FILL = 4, SCAN_CHUNK = 4, SCAN_CHUNKS = 64;
 void scan_plan(const wtconv_scan_desc* d, int* chunks, int* chunk_tiles) {
   const long long rows = (long long)d->B * scan_blocks(d) * d->G, tiles = ceil_div(d->T, SCAN_T);
   long long n = 1;
-  if (rows * 2 <= SMS * SCAN_FILL) n = std::max(1ll, std::min(SMS * SCAN_FILL / rows, tiles / SCAN_CHUNK));
+  if (rows * 2 <= SMS * SCAN_FILL) n = std::max(1ll, std::min(std::min<long long>(SCAN_CHUNKS, SMS * SCAN_FILL / rows), tiles / SCAN_CHUNK));
   *chunk_tiles = (int)ceil_div(tiles, n);
   *chunks = (int)ceil_div(tiles, *chunk_tiles);
 }
@@ -265,20 +267,28 @@ template <typename K> wtconv_status allow_smem(K kernel, size_t bytes) {
              : WTCONV_ERR_CUDA;
 }
 
-// Calls f with the warps of a block: SCAN_J states each.
-template <typename F> wtconv_status with_warps(int N, F f) {
-  if (N <= SCAN_J) return f(Int<1>());
-  if (N <= 2 * SCAN_J) return f(Int<2>());
-  if (N <= 4 * SCAN_J) return f(Int<4>());
-  if (N <= 8 * SCAN_J) return f(Int<8>());
-  return f(Int<16>());
+// Calls f with the warps of a block: SCAN_J states each, but up to four where
+// so few blocks leave an SM with less than four warps.  Warps without a state
+// still take their share of the tokens in A and C, which is most of the work of
+// a block of four states (8x77x121 bf16, N = 4: gradients 70 us in blocks of
+// one warp, 39 us in blocks of four).
+template <typename F> wtconv_status with_warps(int N, long long blocks, F f) {
+  int W = N <= SCAN_J ? 1 : (N <= 2 * SCAN_J ? 2 : (N <= 4 * SCAN_J ? 4 : (N <= 8 * SCAN_J ? 8 : 16)));
+  while (W < 4 && blocks * W < SMS * 4) W *= 2;
+  switch (W) {
+    case 1: return f(Int<1>());
+    case 2: return f(Int<2>());
+    case 4: return f(Int<4>());
+    case 8: return f(Int<8>());
+    default: return f(Int<16>());
+  }
 }
 static_assert(WTCONV_SCAN_MAX_N == 16 * SCAN_J, "a block has at most 16 warps");
 
 template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>& p, cudaStream_t st) {
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
-  return with_warps(p.N, [&](auto W) {
+  return with_warps(p.N, blocks, [&](auto W) {
     const size_t smem = ScanSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
     TRY((allow_smem(scan_forward_kernel<IO, MODE, W.value>, smem)));
     scan_forward_kernel<IO, MODE, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
@@ -348,7 +358,7 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
   TRY((run_scan_pass<IO, SCAN_CKPT>(p, st)));
   if (p.chunks > 1) TRY((run_scan_pass<IO, SCAN_GRAD_ENDS>(p, st)));
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks, parts = (long long)p.chunks * p.B;
-  TRY(with_warps(p.N, [&](auto W) {
+  TRY(with_warps(p.N, blocks, [&](auto W) {
     const size_t smem = ScanGradSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
     TRY((allow_smem(scan_backward_kernel<IO, W.value>, smem)));
     scan_backward_kernel<IO, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
@@ -377,7 +387,7 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
 
 // -------------------------------------------------------------------- norm
 wtconv_status check_norm(const wtconv_norm_desc* d) {
-  if (!d || d->B <= 0 || d->T <= 0 || d->C <= 0 || !dtype_ok(d->io) || !dtype_ok(d->res) || !(d->eps >= 0.f))
+  if (!d || d->B <= 0 || d->T <= 0 || d->T > MAX_TOKENS || d->C <= 0 || !dtype_ok(d->io) || !dtype_ok(d->res) || !(d->eps >= 0.f))
     return WTCONV_ERR_ARG;
   if ((long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
   return d->C > WTCONV_NORM_MAX_C || (long long)d->B * d->T > INT_MAX ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
@@ -684,10 +694,13 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
       return norm_variant<IO>(C, vec, [&](auto v, auto nv, auto wide, int threads) {
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         const int blocks = norm_blocks(desc, threads, v.value * nv.value <= 8 ? NORM_THREADS : 512);
-        if (v.value * nv.value <= 8 && threads <= 256)
-          norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 256><<<blocks, threads, 0, st>>>(a);
-        else
-          norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 512><<<blocks, threads, 0, st>>>(a);
+        if constexpr (v.value * nv.value <= 8) {
+          if (threads <= 256) {
+            norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 256><<<blocks, threads, 0, st>>>(a);
+            return launched();
+          }
+        }
+        norm_forward_kernel<IO, RES, v.value, nv.value, wide.value, 512><<<blocks, threads, 0, st>>>(a);
         return launched();
       });
     });

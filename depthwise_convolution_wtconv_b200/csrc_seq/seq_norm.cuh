@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
   };
   if (AHEAD) load(), then.next();
   int turn = 0;
-  for (; now.left > 0; now.next(), turn ^= 1) {
+  for (; now.left > 0; now.next()) {
     const int b = now.b, t = now.t;
     const bool live = t < row_length(a.lengths, b, a.T);
     if (!AHEAD) load(), then.next();
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_
       }
       continue;
     }
+    turn ^= 1;  // rows without barriers do not count
     float n1 = 1.f, n2 = 1.f;
     if (a.w) {
       float q[1] = {0.f};
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
   };
   if (AHEAD) load(), then.next();
   int turn = 0;
-  for (; now.left > 0; now.next(), turn ^= 1) {
+  for (; now.left > 0; now.next()) {
     const int b = now.b, t = now.t;
     const bool live = t < row_length(a.lengths, b, a.T);
     if (!AHEAD) load(), then.next();
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(NormArgs<IO, RES>
       }
       continue;
     }
+    turn ^= 1;  // rows without barriers do not count
     float n1 = 1.f;
     if (a.w) {
       float s[1] = {total(uu)};

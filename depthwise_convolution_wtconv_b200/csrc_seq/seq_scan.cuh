@@ -180,17 +180,11 @@ template <typename IO, int W, int R> struct TileCopies {
   }
 };
 
-// b, c or both of a tile, [t][n], as fp32 [n][t]: a thread per token and two states.
+// b, c or both of a tile, [t][n] with n a multiple of four, as fp32 [n][t]: a
+// thread per token and two states.
 template <typename IO, int W, bool HAS_B, bool HAS_C>
 __device__ __forceinline__ void transpose_tiles(const IO* b, const IO* c, int N, float* tb, float* tc) {
   const int t = threadIdx.x % SCAN_T;
-  if (N & 1) {
-    for (int n = threadIdx.x / SCAN_T; n < N; n += W * 32 / SCAN_T) {
-      if (HAS_B) tb[n * SCAN_LD + t] = to_f<IO>(b[t * N + n]);
-      if (HAS_C) tc[n * SCAN_LD + t] = to_f<IO>(c[t * N + n]);
-    }
-    return;
-  }
   for (int n = threadIdx.x / SCAN_T * 2; n < N; n += W * 64 / SCAN_T) {
     if (HAS_B) {
       const Pack<IO, 2> u = *reinterpret_cast<const Pack<IO, 2>*>(b + t * N + n);

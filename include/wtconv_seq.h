@@ -75,7 +75,8 @@ typedef struct {
   long long batch_stride, token_stride;
 } wtconv_rows;
 
-/* B batch rows of T tokens of C channels, k taps, silu after it or not. */
+/* B batch rows of T tokens (at most 2^30) of C channels, k taps, silu after it
+ * or not. */
 typedef struct {
   int B, T, C, k;
   wtconv_dtype io;

@@ -563,3 +563,82 @@ def test_block_for_serving(cuda_ok, io):
         assert rel(torch.stack([o[i] for o, _ in got]), want[i, n[i]: n[i] + more]) < tol
         assert rel(torch.stack([r[i] for _, r in got]), want_res[i, n[i]: n[i] + more]) < tol
     assert rel(s1, states[0]) < tol and rel(s2, states[1]) < tol
+
+
+def _far(t):
+    """... in a batch whose rows lie so far apart that the last one begins behind 2^31 elements."""
+    row = t[0].numel()
+    buf = torch.empty(2 * ((1 << 30) + 8) + row, dtype=t.dtype, device=t.device)
+    far = buf.as_strided((3, *t.shape[1:]), ((1 << 30) + 8, *t.stride()[1:]))
+    far.copy_(t)
+    return far
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_offsets_beyond_32_bits(cuda_ok, op):
+    """Inputs whose last batch row begins behind 2^31 elements give what dense ones give."""
+    want, got = _calls("bf16", C=16, T=20)[op](), _calls("bf16", C=16, T=20, view=lambda t: _far(t.contiguous()))[op]()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_token_strides_beyond_32_bits_in_all(cuda_ok):
+    """Tokens 2^29 elements apart: the fifth begins at 2^31."""
+    x = sc.normal(sc.gen(3), 1, 5, 40, dt=torch.bfloat16).cuda()
+    buf = torch.empty(4 * (1 << 29) + 40, dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((1, 5, 40), (0, 1 << 29, 1))
+    far.copy_(x)
+    w = sc.normal(sc.gen(4), 40, 4).cuda()
+    out = torch.empty_like(buf).as_strided((1, 5, 40), (0, 1 << 29, 1))
+    y, _ = wt.causal_forward(x, w)
+    wt.causal_forward(far, w, y=out)
+    assert torch.equal(y, out)
+    a, bc = -torch.ones(40, 8, device="cuda"), sc.normal(sc.gen(5), 1, 5, 8, dt=torch.bfloat16).cuda()
+    y, _ = wt.scan_forward(x, x, a, bc, bc)
+    wt.scan_forward(far, far, a, bc, bc, y=out)
+    assert torch.equal(y, out)
+    ones = torch.ones(40, device="cuda")
+    y, _ = wt.norm_forward(x, ones)
+    wt.norm_forward(far, ones, y=out)
+    assert torch.equal(y, out)
+
+
+@pytest.mark.parametrize("T", [300, 2500])
+@pytest.mark.parametrize("C,G,N,io", [(30, 2, 13, "bf16"), (64, 1, 16, "f32"), (33, 1, 4, "bf16")])
+def test_scan_gradients_of_cut_rows(cuda_ok, T, C, G, N, io):
+    """Rows cut into chunks, an empty one, a whole one and one that ends inside: the gradients of each row are those of the
+    row on its own, in a batch large enough not to be cut."""
+    B = 3
+    s = scan_case(B, T, C, N, io, G=G, seed=9)
+    n = torch.tensor([T, 0, T // 3 + 5], dtype=torch.int32)
+    d = cuda({**s, "lengths": n})
+    names = ("x", "dt", "b", "c", "z", "dy", "state", "dstate")
+    run = lambda d: wt.scan_backward(d["x"], d["dt"], d["a"], d["b"], d["c"], d["dy"], d["d"], d["z"], d["dt_bias"], state=d["state"],
+                                     lengths=d["lengths"], dstate=d["dstate"])
+    cut = run(d)
+    many = 300  # copies of the batch: more rows than would be cut
+    big = run({**d, **{m: d[m].repeat(many, *[1] * (d[m].dim() - 1)) for m in names}, "lengths": d["lengths"].repeat(many)})
+    for m in ("dx", "ddt", "db", "dc", "dz", "dstate"):
+        a, b = cut[m].double(), big[m][:B].double()
+        tol = 2 * sc.HALF[cut[m].dtype] + 2.0 ** -14  # 2^-21 for each of the about 100 tokens that a state lasts
+        assert torch.allclose(a, b, rtol=tol, atol=tol * float(b.abs().max())), m
+    for m in ("da", "dd", "ddt_bias"):
+        a, b = cut[m].double(), big[m].double() / many
+        assert float((a - b).norm() / b.norm()) < 2.0 ** -14, m
+
+
+@pytest.mark.parametrize("parts", [dict(gate=False), dict(w=False, gate=False, res="f32")], ids=["post", "pre"])
+def test_norm_of_rows_between_empty_ones(cuda_ok, parts):
+    """Many short rows, most of them empty, through blocks that go on from row to row with one sum over the block each."""
+    B, T, C = 900, 4, 2048
+    s = norm_case(B, T, C, "bf16", **parts, seed=2)
+    s["lengths"] = torch.tensor([(0, 1, 0, 4, 0, 0, 2)[i % 7] for i in range(B)], dtype=torch.int32)
+    d = cuda(s)
+    args = (d["x"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"])
+    y, _ = wt.norm_forward(*args, lengths=d["lengths"])
+    whole, _ = wt.norm_forward(*args)
+    live = (torch.arange(T, device="cuda") < d["lengths"][:, None])[..., None]
+    assert torch.equal(y, torch.where(live, whole, 0))
+    g = wt.norm_backward(d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], dres=d["dres"], lengths=d["lengths"])
+    h = wt.norm_backward(d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], dres=d["dres"])
+    assert torch.equal(g["dx"], torch.where(live, h["dx"], 0))
