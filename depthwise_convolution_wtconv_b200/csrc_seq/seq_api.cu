@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <initializer_list>
 #include <type_traits>
 
 #include "seq_causal.cuh"
@@ -52,6 +53,18 @@ wtconv_status check_ws(const void* ws, size_t have, size_t need) {
   if (!ws || have < need) return WTCONV_ERR_WORKSPACE;
   return aligned(ws, 16) ? WTCONV_OK : WTCONV_ERR_ALIGN;
 }
+
+// Whether an output begins where an input does.  Threads read what others
+// write then (the convolution's strips, the scan's chunks), so the call is
+// refused; the single-token calls and the norms read every value before its
+// own thread writes there.
+template <typename A, typename B> bool begins_with(std::initializer_list<const A*> outs, std::initializer_list<const B*> ins) {
+  for (const A* o : outs)
+    for (const B* i : ins)
+      if (o && i && o->data == i->data) return true;
+  return false;
+}
+typedef wtconv_rows Rw;
 
 #define TRY(call)                                   \
   do {                                              \
@@ -476,6 +489,7 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ptr(state, e, false));
   TRY(check_ptr(state_out, e, false));
+  if (begins_with<Rw, Rw>({y}, {x})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -514,6 +528,7 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
   TRY(check_ptr(dstate_out, e, false));
   TRY(check_ptr(dstate, e, false));
   TRY(check_ws(ws, ws_bytes, causal_ws(desc)));
+  if (begins_with<Rw, Rw>({dx}, {x, dy})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -580,6 +595,7 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
   TRY(check_ptr(state_out, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 0)));
+  if (begins_with<Rw, Rw>({y}, {x, dt, b, c, z})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -622,6 +638,7 @@ wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_ro
   TRY(check_ptr(dstate, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 1)));
+  if (begins_with<Rw, Rw>({dx, ddt, db, dc, dz}, {x, dt, b, c, z, dy})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -653,15 +670,15 @@ wtconv_status wtconv_scan_step(const wtconv_scan_desc* desc, const wtconv_rows* 
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
     p.y = rows_of<IO>(y);
     p.state_out = state;
-    p.blocks = (int)ceil_div(p.C, 32);
-    const long long blocks = (long long)p.blocks * p.B;
-    if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
+    // blocks of 128 threads to fill the SMs, each with its share of the rows
+    const long long columns = ceil_div(p.C, 32);
+    const dim3 grid((unsigned)columns, (unsigned)std::min<long long>({p.B, 65535, std::max(1ll, SMS * 16 / columns)}));
     const size_t e = sizeof(IO);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p.N % 4 == 0 && wide(a, 4, 4) && wide(state, 4, 4) && wide(b, 4, e, p.B, 1) && wide(c, 4, e, p.B, 1))
-      scan_step_kernel<IO, true><<<(unsigned)blocks, 128, 0, st>>>(p, active);
+      scan_step_kernel<IO, true><<<grid, 128, 0, st>>>(p, active);
     else
-      scan_step_kernel<IO, false><<<(unsigned)blocks, 128, 0, st>>>(p, active);
+      scan_step_kernel<IO, false><<<grid, 128, 0, st>>>(p, active);
     return launched();
   });
 }

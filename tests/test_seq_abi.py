@@ -185,3 +185,24 @@ _CALLS = {
 def test_every_binding_refuses_cpu_tensors(name):
     with pytest.raises(TypeError, match="CUDA tensor"):
         _CALLS[name]()
+
+
+def test_outputs_in_place_of_inputs_are_refused(lib):
+    """A convolution or scan whose output begins where an input does would read what it has written."""
+    far = lambda k: R(FAKE + (k << 32))
+    d = causal_desc()
+    assert lib.wtconv_causal_forward(d, far(1), FAKE, None, None, None, far(1), None, None) == ARG
+    need = lib.wtconv_causal_workspace_size(d)
+    for dx in (1, 2):
+        assert lib.wtconv_causal_backward(d, far(1), far(2), FAKE, None, None, None, None, far(dx), FAKE, None, None, FAKE, need,
+                                          None) == ARG
+    s = scan_desc()
+    for k in range(1, 6):
+        assert lib.wtconv_scan_forward(s, far(1), far(2), FAKE, far(3), far(4), None, far(5), None, None, None, far(k), None, FAKE,
+                                       1 << 40, None) == ARG
+    need = lib.wtconv_scan_workspace_size(s, 1)
+    outs = dict(dx=far(11), ddt=far(12), db=far(13), dc=far(14), dz=far(15))
+    for m in outs:
+        o = {**outs, m: far(6)}
+        assert lib.wtconv_scan_backward(s, far(1), far(2), FAKE, far(3), far(4), None, far(5), None, None, None, far(6), None, o["dx"],
+                                        o["ddt"], FAKE, o["db"], o["dc"], None, o["dz"], None, None, FAKE, need, None) == ARG
