@@ -642,3 +642,60 @@ def test_norm_of_rows_between_empty_ones(cuda_ok, parts):
     g = wt.norm_backward(d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], dres=d["dres"], lengths=d["lengths"])
     h = wt.norm_backward(d["x"], d["dy"], d["w"], d["gate"], d["res"], d["scale"], d["w_res"], dres=d["dres"])
     assert torch.equal(g["dx"], torch.where(live, h["dx"], 0))
+
+
+# blocks of 1, 2, 4, 8 and 16 warps (a warp per four states, and up to four where blocks are few), tokens shared out among them
+SCAN_WARPS = [
+    dict(B=40, T=20, C=480, N=4, io="bf16"),                             # 600 blocks of one warp
+    dict(B=20, T=21, C=480, N=7, io="f32", ragged=True),                 # 300 of two, states copied to eight
+    dict(B=2, T=35, C=40, N=24, io="bf16", ragged=True),                 # eight warps, six with states
+    dict(B=2, T=35, C=40, N=32, io="f32"),
+    dict(B=2, T=50, C=24, N=33, io="bf16", G=3, z=False),                # sixteen, 36 states after the copy
+    dict(B=1, T=4100, C=8, N=16, io="f32", ragged=False),                # as many chunks as there may be
+]
+
+
+@pytest.mark.parametrize("case", SCAN_WARPS, ids=_name)
+def test_scan_in_blocks_of_all_sizes(cuda_ok, case):
+    s = scan_case(**case, seed=21)
+    d = cuda(s)
+    args = (d["x"], d["dt"], d["a"], d["b"], d["c"])
+    y, state = wt.scan_forward(*args, d["d"], d["z"], d["dt_bias"], state=d["state"], lengths=d["lengths"])
+    g = wt.scan_backward(*args, d["dy"], d["d"], d["z"], d["dt_bias"], state=d["state"], lengths=d["lengths"], dstate=d["dstate"])
+    want, size = scan_oracle(s, grads=True), scan_oracle(s, grads=True, mag=True)
+    ops = scan_ops(case["B"], min(case["T"], 600), case["C"], case["N"]) + case["T"] / 8  # a state outlasts 600 tokens by less than that
+    check(y, want["y"], size["y"], ops, "y")
+    check(state, want["state"], size["state"], ops, "state")
+    for m in ("dx", "ddt", "da", "db", "dc", "dd", "dz", "ddt_bias", "dstate"):
+        check(g[m], None if m == "dz" and s["z"] is None else want[m], size[m], 2 * ops, m)
+
+
+@pytest.mark.parametrize("N", [4, 8, 24, 64])
+def test_scan_step_of_many_rows(cuda_ok, N):
+    """More rows than blocks along them, some switched off: the same as one token of the forward pass."""
+    s = scan_case(500, 1, 100, N, "bf16", seed=22)
+    d = cuda(s)
+    active = (torch.arange(500, device="cuda") % 3 != 0).to(torch.int32)
+    want, after = wt.scan_forward(d["x"], d["dt"], d["a"], d["b"], d["c"], d["d"], d["z"], d["dt_bias"], state=d["state"],
+                                  lengths=active)
+    held = d["state"].clone()
+    one = lambda m: d[m][:, 0]
+    y = wt.scan_step(one("x"), one("dt"), held, d["a"], one("b"), one("c"), d["d"], one("z"), d["dt_bias"], active=active)
+    assert torch.allclose(y.float(), want[:, 0].float(), rtol=2.0 ** -7, atol=1e-6 * float(want.abs().max()))  # a step of bf16
+    assert torch.allclose(held, after, rtol=2.0 ** -20, atol=2.0 ** -20 * float(after.abs().max()))
+    off = ~active.bool()
+    assert torch.equal(held[off], d["state"][off]) and not y[off].any()
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_two_calls_at_once(cuda_ok, op):
+    """The same call on two streams at the same time, each with workspaces of its own."""
+    call = _calls("f32", C=96, T=400)[op]
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [call(stream=streams[k % 2]) for k in range(6)]
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(want, g):
+            assert torch.equal(a, b)
