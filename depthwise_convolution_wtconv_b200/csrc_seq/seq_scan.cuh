@@ -906,15 +906,15 @@ struct ScanSumFloats {
 template <typename IO> __global__ void __launch_bounds__(256) scan_sums_kernel(const ScanSums<IO> p) {
   const long long x = blockIdx.x;
   if (x < p.first[1])
-    sum_block(p.part[0], p.P[0], p.n[0], p.n[0], x, ScanSumRows<IO>{p.db, p.B, p.T, p.N});
+    sum_block<8>(p.part[0], p.P[0], p.n[0], p.n[0], x, ScanSumRows<IO>{p.db, p.B, p.T, p.N});
   else if (x < p.first[2])
-    sum_block(p.part[1], p.P[1], p.n[1], p.n[1], x - p.first[1], ScanSumRows<IO>{p.dc, p.B, p.T, p.N});
+    sum_block<8>(p.part[1], p.P[1], p.n[1], p.n[1], x - p.first[1], ScanSumRows<IO>{p.dc, p.B, p.T, p.N});
   else if (x < p.first[3])
-    sum_block(p.part[2], p.P[2], p.n[2], p.n[2], x - p.first[2], ScanSumFloats{p.to[2]});
+    sum_block<8>(p.part[2], p.P[2], p.n[2], p.n[2], x - p.first[2], ScanSumFloats{p.to[2]});
   else if (x < p.first[4])
-    sum_block(p.part[3], p.P[3], p.n[3], p.n[3], x - p.first[3], ScanSumFloats{p.to[3]});
+    sum_block<8>(p.part[3], p.P[3], p.n[3], p.n[3], x - p.first[3], ScanSumFloats{p.to[3]});
   else
-    sum_block(p.part[4], p.P[4], p.n[4], p.n[4], x - p.first[4], ScanSumFloats{p.to[4]});
+    sum_block<8>(p.part[4], p.P[4], p.n[4], p.n[4], x - p.first[4], ScanSumFloats{p.to[4]});
 }
 
 // One token of every row: four threads share a channel's states and join their
