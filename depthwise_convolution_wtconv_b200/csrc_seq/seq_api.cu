@@ -58,13 +58,13 @@ wtconv_status check_ws(const void* ws, size_t have, size_t need) {
 // write then (the convolution's strips, the scan's chunks), so the call is
 // refused; the single-token calls and the norms read every value before its
 // own thread writes there.
-template <typename A, typename B> bool begins_with(std::initializer_list<const A*> outs, std::initializer_list<const B*> ins) {
-  for (const A* o : outs)
-    for (const B* i : ins)
+typedef std::initializer_list<const wtconv_rows*> RowsList;
+bool begins_with(RowsList outs, RowsList ins) {
+  for (const wtconv_rows* o : outs)
+    for (const wtconv_rows* i : ins)
       if (o && i && o->data == i->data) return true;
   return false;
 }
-typedef wtconv_rows Rw;
 
 #define TRY(call)                                   \
   do {                                              \
@@ -489,7 +489,7 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ptr(state, e, false));
   TRY(check_ptr(state_out, e, false));
-  if (begins_with<Rw, Rw>({y}, {x})) return WTCONV_ERR_ARG;
+  if (begins_with({y}, {x})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -528,7 +528,7 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
   TRY(check_ptr(dstate_out, e, false));
   TRY(check_ptr(dstate, e, false));
   TRY(check_ws(ws, ws_bytes, causal_ws(desc)));
-  if (begins_with<Rw, Rw>({dx}, {x, dy})) return WTCONV_ERR_ARG;
+  if (begins_with({dx}, {x, dy})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -595,7 +595,7 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
   TRY(check_ptr(state_out, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 0)));
-  if (begins_with<Rw, Rw>({y}, {x, dt, b, c, z})) return WTCONV_ERR_ARG;
+  if (begins_with({y}, {x, dt, b, c, z})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -638,7 +638,7 @@ wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_ro
   TRY(check_ptr(dstate, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 1)));
-  if (begins_with<Rw, Rw>({dx, ddt, db, dc, dz}, {x, dt, b, c, z, dy})) return WTCONV_ERR_ARG;
+  if (begins_with({dx, ddt, db, dc, dz}, {x, dt, b, c, z, dy})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);

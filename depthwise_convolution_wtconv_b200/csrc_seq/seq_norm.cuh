@@ -1,14 +1,13 @@
 // Norms before and after a block with its gate and residual scale.
 //
 // A block of threads holds one row at a time in registers, NV chunks of V
-// channels a thread: each input is read once and each output
-// written once.  A block goes through its rows with the parameters of its
-// channels, and for the gradients the sums over the rows, in registers; where
-// these fit (8 values a thread) the next row's inputs are on their way while a
-// row is worked on.
+// channels a thread: each input is read once and each output written once.  A
+// block goes through its rows with the parameters of its channels, and for the
+// gradients the sums over the rows, in registers; where these fit (8 values a
+// thread) the next row's inputs are on their way while a row is worked on.
 //
 // Memory is the floor.  8x2048x2048 bf16 with an fp32 residual and all parts:
-// forward 87 us (5.4 TB/s, 83% of the floor), gradients 178 us (4.1 TB/s, 63%;
+// forward 88 us (5.3 TB/s, 82% of the floor), gradients 178 us (4.1 TB/s, 63%;
 // 126 registers leave 16 warps an SM).  One row a block at a time, loads only
 // when needed, took 141 and 487 us.
 #pragma once
@@ -102,9 +101,8 @@ template <int V, bool WIDE> struct Cols {
   }
 };
 
-// The fp32 parameters of a thread's channels: kept in registers, or loaded
-// where they are used.
-// (one where there is none; the product of two)
+// The fp32 parameters of a thread's channels, the product of two (one where
+// there is none): kept in registers, or loaded where they are used.
 template <int V, int NV, bool WIDE, bool KEEP> struct Params {
   const float *p, *p2;
   Vals<V> kept[KEEP ? NV : 1];
