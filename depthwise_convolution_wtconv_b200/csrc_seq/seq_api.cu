@@ -110,7 +110,7 @@ size_t causal_ws(const wtconv_causal_desc* d) {
 template <typename IO> CausalArgs<IO> causal_args(const wtconv_causal_desc* d, const wtconv_rows* x, const float* w,
                                                   const float* bias) {
   CausalArgs<IO> a = {};
-  a.x = rows_of<IO>(x);
+  a.x = rows_of<IO>(x, d->T);
   a.w = w;
   a.bias = bias;
   a.B = d->B;
@@ -237,11 +237,11 @@ ScanArgs<IO> scan_args(const wtconv_scan_desc* d, const wtconv_rows* x, const wt
                        const wtconv_rows* b, const wtconv_rows* c, const float* skip, const wtconv_rows* z,
                        const float* dt_bias) {
   ScanArgs<IO> p = {};
-  p.x = rows_of<IO>(x);
-  p.dt = rows_of<IO>(dt);
-  p.z = rows_of<IO>(z);
-  p.b = rows_of<IO>(b);
-  p.c = rows_of<IO>(c);
+  p.x = rows_of<IO>(x, d->T);
+  p.dt = rows_of<IO>(dt, d->T);
+  p.z = rows_of<IO>(z, d->T);
+  p.b = rows_of<IO>(b, d->T);
+  p.c = rows_of<IO>(c, d->T);
   p.a = a;
   p.d = skip;
   p.dt_bias = dt_bias;
@@ -378,7 +378,7 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
     return launched();
   }));
   ScanSums<IO> sums = {};
-  sums.db = rows_of<IO>(db), sums.dc = rows_of<IO>(dc);
+  sums.db = rows_of<IO>(db, p.T), sums.dc = rows_of<IO>(dc, p.T);
   sums.B = p.B, sums.T = p.T, sums.N = p.N;
   long long first = 0;
   int k = 0;
@@ -432,9 +432,9 @@ template <typename IO, typename RES>
 NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, const wtconv_rows* gate, const float* w,
                             const wtconv_rows* res, const float* scale, const float* w_res, const int* lengths) {
   NormArgs<IO, RES> a = {};
-  a.x = rows_of<IO>(x);
-  a.gate = rows_of<IO>(gate);
-  a.res = rows_of<RES>(res);
+  a.x = rows_of<IO>(x, d->T);
+  a.gate = rows_of<IO>(gate, d->T);
+  a.res = rows_of<RES>(res, d->T);
   a.w = w;
   a.scale = scale;
   a.w_res = w_res;
@@ -493,7 +493,7 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
-    a.y = rows_of<IO>(y);
+    a.y = rows_of<IO>(y, T);
     a.state = static_cast<const IO*>(state);
     a.state_out = static_cast<IO*>(state_out);
     a.lengths = lengths;
@@ -532,8 +532,8 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
-    a.dy = rows_of<IO>(dy);
-    a.dx = rows_of<IO>(dx);
+    a.dy = rows_of<IO>(dy, T);
+    a.dx = rows_of<IO>(dx, T);
     a.state = static_cast<const IO*>(state);
     a.dstate_out = static_cast<const IO*>(dstate_out);
     a.dstate = static_cast<IO*>(dstate);
@@ -570,7 +570,7 @@ wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_ro
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
-    a.y = rows_of<IO>(y);
+    a.y = rows_of<IO>(y, 1);
     a.state_out = static_cast<IO*>(state);
     constexpr int V = 4;
     const bool vec = C % V == 0 && wide(w, 4, 4) && wide(x, V, e, B, 1) && wide(y, V, e, B, 1) && wide(state, V, e);
@@ -599,7 +599,7 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
-    p.y = rows_of<IO>(y);
+    p.y = rows_of<IO>(y, desc->T);
     p.state = state;
     p.state_out = state_out;
     p.lengths = lengths;
@@ -642,10 +642,10 @@ wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_ro
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
-    p.dy = rows_of<IO>(dy);
-    p.dx = rows_of<IO>(dx);
-    p.ddt = rows_of<IO>(ddt);
-    p.dz = rows_of<IO>(dz);
+    p.dy = rows_of<IO>(dy, T);
+    p.dx = rows_of<IO>(dx, T);
+    p.ddt = rows_of<IO>(ddt, T);
+    p.dz = rows_of<IO>(dz, T);
     p.state = state;
     p.dstate_out = dstate_out;
     p.dstate = dstate;
@@ -668,7 +668,7 @@ wtconv_status wtconv_scan_step(const wtconv_scan_desc* desc, const wtconv_rows* 
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
-    p.y = rows_of<IO>(y);
+    p.y = rows_of<IO>(y, 1);
     p.state_out = state;
     // blocks of 128 threads to fill the SMs, each with its share of the rows
     const long long columns = ceil_div(p.C, 32);
@@ -702,8 +702,8 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
     return with_io(desc->res, [&](auto rio) {
       using RES = decltype(rio);
       NormArgs<IO, RES> a = norm_args<IO, RES>(desc, x, gate, w, res, scale, w_res, lengths);
-      a.y = rows_of<IO>(y);
-      a.res_out = rows_of<RES>(res_out);
+      a.y = rows_of<IO>(y, T);
+      a.res_out = rows_of<RES>(res_out, T);
       constexpr int V = sizeof(IO) == 2 ? 8 : 4;
       const bool vec = C % V == 0 && wide(x, V, sizeof(IO), B, T) && wide(gate, V, sizeof(IO), B, T) &&
                        wide(y, V, sizeof(IO), B, T) && wide(res, V, sizeof(RES), B, T) &&
@@ -751,11 +751,11 @@ wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_ro
     return with_io(desc->res, [&](auto rio) {
       using RES = decltype(rio);
       NormArgs<IO, RES> a = norm_args<IO, RES>(desc, x, gate, w, res, scale, w_res, lengths);
-      a.dy = rows_of<IO>(dy);
-      a.dres_out = rows_of<RES>(dres_out);
-      a.dx = rows_of<IO>(dx);
-      a.dgate = rows_of<IO>(dgate);
-      a.dres = rows_of<RES>(dres);
+      a.dy = rows_of<IO>(dy, T);
+      a.dres_out = rows_of<RES>(dres_out, T);
+      a.dx = rows_of<IO>(dx, T);
+      a.dgate = rows_of<IO>(dgate, T);
+      a.dres = rows_of<RES>(dres, T);
       a.part = static_cast<float*>(ws);
       constexpr int V = sizeof(IO) == 2 ? 8 : 4;
       const size_t e = sizeof(IO), re = sizeof(RES);

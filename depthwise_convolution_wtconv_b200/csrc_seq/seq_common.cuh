@@ -26,9 +26,12 @@ template <typename IO> struct Rows {
   __device__ __forceinline__ IO* at(int b, long long t) const { return p + b * sb + t * st; }
 };
 
-template <typename IO> inline Rows<IO> rows_of(const wtconv_rows* r) {
+// Rows of one token have no token stride: what the caller holds there may be
+// anything, and kernels that copy whole tiles form the addresses of the tokens
+// that are not there too (a copy of no bytes still wants an aligned one).
+template <typename IO> inline Rows<IO> rows_of(const wtconv_rows* r, int T) {
   if (!r) return Rows<IO>{nullptr, 0, 0};
-  return Rows<IO>{static_cast<IO*>(r->data), r->batch_stride, r->token_stride};
+  return Rows<IO>{static_cast<IO*>(r->data), r->batch_stride, T > 1 ? r->token_stride : 0};
 }
 
 // V consecutive channels in accesses of up to 16 bytes, which they are aligned
