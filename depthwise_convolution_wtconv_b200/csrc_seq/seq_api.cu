@@ -273,9 +273,13 @@ wtconv_status check_scan_inputs(const wtconv_scan_desc* d, const wtconv_rows* x,
   return check_ptr(dt_bias, 4, false);
 }
 
-template <typename K> wtconv_status allow_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return WTCONV_OK;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
+// Lets a kernel have `most` bytes of shared memory.  The limit belongs to the
+// kernel, and other host threads launch it with other counts of states, so
+// `most` is what the kernel needs at the most states that its blocks hold: every
+// call sets the same.
+template <typename K> wtconv_status allow_smem(K kernel, size_t most) {
+  if (most <= 48 * 1024) return WTCONV_OK;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess
              ? WTCONV_OK
              : WTCONV_ERR_CUDA;
 }
@@ -302,8 +306,9 @@ template <typename IO, int MODE> wtconv_status run_scan_pass(const ScanArgs<IO>&
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks;
   if (!grid_ok(blocks)) return WTCONV_ERR_UNSUPPORTED;
   return with_warps(p.N, blocks, [&](auto W) {
-    const size_t smem = ScanSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
-    TRY((allow_smem(scan_forward_kernel<IO, MODE, W.value>, smem)));
+    auto smem_of = [&](int states) { return (size_t)(ScanSmem<IO>(nullptr, states, W.value).end - (char*)nullptr); };
+    const size_t smem = smem_of(p.states);
+    TRY((allow_smem(scan_forward_kernel<IO, MODE, W.value>, smem_of(W.value * SCAN_J))));
     scan_forward_kernel<IO, MODE, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
   });
@@ -372,8 +377,9 @@ wtconv_status run_scan_backward(const wtconv_scan_desc* d, ScanArgs<IO>& p, cons
   if (p.chunks > 1) TRY((run_scan_pass<IO, SCAN_GRAD_ENDS>(p, st)));
   const long long blocks = (long long)p.B * p.blocks * p.G * p.chunks, parts = (long long)p.chunks * p.B;
   TRY(with_warps(p.N, blocks, [&](auto W) {
-    const size_t smem = ScanGradSmem<IO>(nullptr, p.states, W.value).end - (char*)nullptr;
-    TRY((allow_smem(scan_backward_kernel<IO, W.value>, smem)));
+    auto smem_of = [&](int states) { return (size_t)(ScanGradSmem<IO>(nullptr, states, W.value).end - (char*)nullptr); };
+    const size_t smem = smem_of(p.states);
+    TRY((allow_smem(scan_backward_kernel<IO, W.value>, smem_of(W.value * SCAN_J))));
     scan_backward_kernel<IO, W.value><<<(unsigned)blocks, W.value * 32, smem, st>>>(p);
     return launched();
   }));

@@ -6,6 +6,7 @@ import torch
 
 import depthwise_convolution_wtconv_b200 as wt
 import seq_cases as sc
+from depthwise_convolution_wtconv_b200 import _seq
 from seq_cases import cuda, scan_case
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,38 @@ def test_scan_of_one_token_of_rows_at_odd_strides(cuda_ok, io, B, C, N):
         outs.append(dict(g, y=y, state=state))
     for m in outs[0]:
         assert torch.equal(outs[0][m], outs[1][m]), m
+
+
+# ------------------------------------------- calls from two host threads
+def test_scans_of_different_states_from_two_host_threads(cuda_ok):
+    """Four and sixteen states run in the same kernels with shared memory of different sizes; calls from two host threads
+    at once must not take it from one another.  Entries called as the binding calls them, with arguments made ready, so
+    that the threads are inside the library at the same time (the interpreter's lock is not held there)."""
+    import threading
+    B, T, C = 1, 4, 32
+    entry, rows, f32 = _seq._entry("wtconv_scan_forward"), lambda t: _seq._rows(t, "", t.shape, t.dtype, 0), torch.float32
+    calls, kept = [], []
+    for N in (4, 16):
+        d = cuda(scan_case(B, T, C, N, "f32", seed=32))
+        y, st = torch.zeros(B, T, C, device="cuda"), torch.cuda.Stream()
+        b, c = d["b"][:, :, 0], d["c"][:, :, 0]
+        calls.append((_seq._pack_scan(B, T, C, N, 1, 0, 1), rows(d["x"]), rows(d["dt"]), d["a"].data_ptr(), rows(b), rows(c), None,
+                      None, None, None, None, rows(y), None, None, 0, st.cuda_stream))
+        kept.append((d, y, st, wt.scan_forward(d["x"], d["dt"], d["a"], d["b"], d["c"])[0]))
+    torch.cuda.synchronize()
+    answers = [set(), set()]
+    start = threading.Barrier(2)
+
+    def run(i):
+        start.wait()
+        for _ in range(40000):
+            answers[i].add(entry(*calls[i]))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert answers == [{0}, {0}]
+    for _, y, _, want in kept:
+        assert torch.equal(y, want)
