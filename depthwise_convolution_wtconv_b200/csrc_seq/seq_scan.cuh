@@ -266,13 +266,22 @@ template <typename IO> __device__ __forceinline__ ScanPlace scan_place(const Sca
 template <typename IO> __device__ __forceinline__ float scan_first(const ScanArgs<IO>& p, const ScanPlace& w, int n) {
   return p.state ? p.state[((long long)w.b * p.C + w.c) * p.N + n] : 0.f;
 }
+// 2^s h + end, over a chunk.  2^s may be beyond fp32 where h 2^s is not (small
+// states that grow, large ones that shrink): two halves then, and what is zero
+// stays zero.
+__device__ __forceinline__ float scan_join(float s, float h, float end) {
+  if (!(fabsf(s) >= 126.f)) return fmaf(exp2_approx(s), h, end);
+  if (h == 0.f) return end;
+  const float half = exp2_approx(0.5f * s);
+  return fmaf(half, half * h, end);
+}
 // h before the block's chunk: the row's first state joined with the chunks before.
 template <typename IO> __device__ __forceinline__ float scan_start(const ScanArgs<IO>& p, const ScanPlace& w, int n, float a) {
   if (p.chunks == 1) return scan_first(p, w, n);
   float h = p.ends[(((p.chunks - 1ll) * p.B + w.b) * p.N + n) * p.C + w.c];
   for (int k = 0; k < w.chunk; ++k) {
     const long long r = (long long)k * p.B + w.b;
-    h = fmaf(exp2_approx(p.sums[r * p.C + w.c] * a), h, p.ends[(r * p.N + n) * p.C + w.c]);
+    h = scan_join(p.sums[r * p.C + w.c] * a, h, p.ends[(r * p.N + n) * p.C + w.c]);
   }
   return h;
 }
@@ -282,7 +291,7 @@ template <typename IO> __device__ __forceinline__ float scan_grad_start(const Sc
   float e = p.dstate_out ? p.dstate_out[((long long)w.b * p.C + w.c) * p.N + n] : 0.f;
   for (int k = p.chunks - 1; k > w.chunk; --k) {
     const long long r = (long long)k * p.B + w.b;
-    e = fmaf(exp2_approx(p.sums[r * p.C + w.c] * a), e, p.grad_ends[(r * p.N + n) * p.C + w.c]);
+    e = scan_join(p.sums[r * p.C + w.c] * a, e, p.grad_ends[(r * p.N + n) * p.C + w.c]);
   }
   return e;
 }

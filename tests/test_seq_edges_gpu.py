@@ -7,7 +7,7 @@ import torch
 import depthwise_convolution_wtconv_b200 as wt
 import seq_cases as sc
 from depthwise_convolution_wtconv_b200 import _seq
-from seq_cases import cuda, scan_case
+from seq_cases import check, cuda, scan_case, scan_ops, scan_oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,57 @@ def test_scans_of_different_states_from_two_host_threads(cuda_ok):
     assert answers == [{0}, {0}]
     for _, y, _, want in kept:
         assert torch.equal(y, want)
+
+
+# ------------------------------------- chunks over which a state grows
+def _growing(T, dt):
+    """Rows cut into chunks (one row of 8 channels), a > 0, step sizes `dt` as they are; x and dy of one everywhere."""
+    one = lambda *s: torch.ones(*s)
+    return dict(x=one(1, T, 8), dt=dt.reshape(1, T, 1).repeat(1, 1, 8), a=one(8, 4), b=one(1, T, 1, 4), c=one(1, T, 1, 4), d=None, z=None,
+                dt_bias=None, state=None, lengths=None, dy=one(1, T, 8), dstate=None)
+
+
+def _check_scan(s, names):
+    d = cuda(s)
+    args = (d["x"], d["dt"], d["a"], d["b"], d["c"])
+    y, state = wt.scan_forward(*args, softplus=False, state=d["state"])
+    got = dict(wt.scan_backward(*args, d["dy"], softplus=False, state=d["state"], dstate=d["dstate"]), y=y, state=state)
+    want, size = scan_oracle(s, False, True), scan_oracle(s, False, True, mag=True)
+    for m in names:
+        check(got[m], want[m], size[m], 2 * scan_ops(1, s["x"].shape[1], 8, 4), m)
+
+
+def test_scan_state_of_zero_under_growth_beyond_fp32(cuda_ok):
+    """Nothing goes in before the last 20 tokens and no gradient comes from behind the first 20: what stays zero over a
+    chunk stays so, though the chunk's growth, exp(160), is beyond fp32."""
+    s = _growing(2000, torch.full((2000,), 2.0))
+    s["x"][:, :-20] = 0
+    s["dy"][:, 20:] = 0
+    _check_scan(s, ("y", "state", "dx", "ddt", "da", "db", "dc"))
+
+
+def test_scan_growth_beyond_fp32_of_a_small_state(cuda_ok):
+    """A state of 1e-30 grows by exp(100) over the first 80 tokens, and a gradient of 1e-30 by as much on its way back: both
+    are ordinary numbers then.  The exponent is a sum of 80 steps, off by at most 80 roundings of 2^7, 4e-4 in all; the
+    bound is 4e-3."""
+    dt = torch.zeros(2000)
+    dt[:80] = 1.25
+    s = _growing(2000, dt)
+    s["x"].zero_()
+    s["state"] = torch.full((1, 8, 4), 1e-30)
+    s["dy"].zero_()
+    s["dy"][:, -1] = 1e-30
+    _check_scan(s, ("y", "state", "dstate"))
+
+
+def test_scan_decay_beyond_fp32_of_a_large_state(cuda_ok):
+    """... and a state of 1e30 shrinks by exp(-100) to 4e-14."""
+    dt = torch.zeros(2000)
+    dt[:80] = 1.25
+    s = _growing(2000, dt)
+    s["a"] = -s["a"]
+    s["x"].zero_()
+    s["state"] = torch.full((1, 8, 4), 1e30)
+    s["dy"].zero_()
+    s["dy"][:, -1] = 1e30
+    _check_scan(s, ("y", "state", "dstate"))
