@@ -54,16 +54,20 @@ wtconv_status check_ws(const void* ws, size_t have, size_t need) {
   return aligned(ws, 16) ? WTCONV_OK : WTCONV_ERR_ALIGN;
 }
 
-// Whether an output begins where an input does.  Threads read what others
-// write then (the convolution's strips, the scan's chunks), so the call is
-// refused; the single-token calls and the norms read every value before its
-// own thread writes there.
-typedef std::initializer_list<const wtconv_rows*> RowsList;
-bool begins_with(RowsList outs, RowsList ins) {
-  for (const wtconv_rows* o : outs)
-    for (const wtconv_rows* i : ins)
-      if (o && i && o->data == i->data) return true;
+// Whether an output begins where an input does and threads would read there what
+// others have written: such calls are refused.  `in_place`: the call's every
+// value of that input is read by the thread that writes there, before it does
+// (the single-token calls and the norms), which is so if the rows are the same.
+typedef std::initializer_list<const void*> Pointers;
+const void* at(const wtconv_rows* r) { return r ? r->data : nullptr; }
+bool begins_with(Pointers outs, Pointers ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o && o == i) return true;
   return false;
+}
+bool in_place(const wtconv_rows* out, const wtconv_rows* in, int B, int T) {
+  return (B == 1 || out->batch_stride == in->batch_stride) && (T == 1 || out->token_stride == in->token_stride);
 }
 
 #define TRY(call)                                   \
@@ -424,6 +428,21 @@ wtconv_status check_norm_inputs(const wtconv_norm_desc* d, const wtconv_rows* x,
   return check_ptr(lengths, 4, false);
 }
 
+// Whether an output of the norms begins at an input with other rows or of another type.
+struct NormRowsOf {
+  const wtconv_rows* r;
+  wtconv_dtype t;
+};
+bool norm_overlap(const wtconv_norm_desc* d, std::initializer_list<NormRowsOf> outs, std::initializer_list<NormRowsOf> ins,
+                  Pointers params) {
+  for (const NormRowsOf& o : outs) {
+    if (begins_with({at(o.r)}, params)) return true;
+    for (const NormRowsOf& i : ins)
+      if (at(o.r) && at(o.r) == at(i.r) && (o.t != i.t || !in_place(o.r, i.r, d->B, d->T))) return true;
+  }
+  return false;
+}
+
 // Blocks for rows that `threads` threads hold: enough for the SMs' registers,
 // so that each goes through its share of the rows (of the gradients, whose
 // blocks leave a partial sum each, fewer).
@@ -495,7 +514,8 @@ wtconv_status wtconv_causal_forward(const wtconv_causal_desc* desc, const wtconv
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ptr(state, e, false));
   TRY(check_ptr(state_out, e, false));
-  if (begins_with({y}, {x})) return WTCONV_ERR_ARG;
+  const void *const s0 = desc->k > 1 ? state : nullptr, *const s1 = desc->k > 1 ? state_out : nullptr;
+  if (begins_with({at(y), s1}, {at(x), w, bias, lengths}) || begins_with({at(y)}, {s0})) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -534,7 +554,10 @@ wtconv_status wtconv_causal_backward(const wtconv_causal_desc* desc, const wtcon
   TRY(check_ptr(dstate_out, e, false));
   TRY(check_ptr(dstate, e, false));
   TRY(check_ws(ws, ws_bytes, causal_ws(desc)));
-  if (begins_with({dx}, {x, dy})) return WTCONV_ERR_ARG;
+  const bool held = desc->k > 1;
+  if (begins_with({at(dx), held ? dstate : nullptr}, {at(x), at(dy), w, bias, lengths, held ? dstate_out : nullptr}) ||
+      begins_with({at(dx)}, {held ? state : nullptr}))
+    return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -573,6 +596,10 @@ wtconv_status wtconv_causal_step(const wtconv_causal_desc* desc, const wtconv_ro
   TRY(check_ptr(bias, 4, false));
   TRY(check_ptr(active, 4, false));
   TRY(check_ptr(state, e, desc->k > 1));
+  const void* const held = desc->k > 1 ? state : nullptr;
+  if (begins_with({at(y)}, {w, bias, active, held}) || begins_with({held}, {at(x), w, bias, active}) ||
+      (at(y) == at(x) && !in_place(y, x, B, 1)))
+    return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     CausalArgs<IO> a = causal_args<IO>(desc, x, w, bias);
@@ -601,7 +628,8 @@ wtconv_status wtconv_scan_forward(const wtconv_scan_desc* desc, const wtconv_row
   TRY(check_ptr(state_out, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 0)));
-  if (begins_with({y}, {x, dt, b, c, z})) return WTCONV_ERR_ARG;
+  if (begins_with({at(y), state_out}, {at(x), at(dt), at(b), at(c), at(z), a, d, dt_bias, lengths}) || begins_with({at(y)}, {state}))
+    return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -644,7 +672,9 @@ wtconv_status wtconv_scan_backward(const wtconv_scan_desc* desc, const wtconv_ro
   TRY(check_ptr(dstate, 4, false));
   TRY(check_ptr(lengths, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_scan_workspace_size(desc, 1)));
-  if (begins_with({dx, ddt, db, dc, dz}, {x, dt, b, c, z, dy})) return WTCONV_ERR_ARG;
+  const Pointers outs = {at(dx), at(ddt), at(db), at(dc), at(dz)};
+  const Pointers ins = {at(x), at(dt), at(b), at(c), at(z), at(dy), a, d, dt_bias, lengths, dstate_out};
+  if (begins_with(outs, ins) || begins_with(outs, {state}) || begins_with({dstate}, ins)) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -671,6 +701,11 @@ wtconv_status wtconv_scan_step(const wtconv_scan_desc* desc, const wtconv_rows* 
   TRY(check_rows(y, elt(desc->io), desc->B, 1, desc->C, true));
   TRY(check_ptr(state, 4, true));
   TRY(check_ptr(active, 4, false));
+  if (begins_with({at(y)}, {at(b), at(c), a, d, dt_bias, active, state}) ||
+      begins_with({state}, {at(x), at(dt), at(b), at(c), at(z), a, d, dt_bias, active}))
+    return WTCONV_ERR_ARG;
+  for (const wtconv_rows* in : {x, dt, z})
+    if (at(y) == at(in) && !in_place(y, in, desc->B, 1)) return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     ScanArgs<IO> p = scan_args<IO>(desc, x, dt, a, b, c, d, z, dt_bias);
@@ -703,6 +738,9 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
   if ((res != nullptr) != (res_out != nullptr) || (!res || w_res ? !y : y != nullptr)) return WTCONV_ERR_ARG;
   if (y) TRY(check_rows(y, elt(desc->io), B, T, C, true));
   if (res_out) TRY(check_rows(res_out, elt(desc->res), B, T, C, true));
+  if (norm_overlap(desc, {{y, desc->io}, {res_out, desc->res}}, {{x, desc->io}, {gate, desc->io}, {res, desc->res}},
+                   {w, scale, w_res, lengths}))
+    return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     return with_io(desc->res, [&](auto rio) {
@@ -752,6 +790,10 @@ wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_ro
   TRY(check_ptr(dscale, 4, false));
   TRY(check_ptr(dw_res, 4, false));
   TRY(check_ws(ws, ws_bytes, wtconv_norm_workspace_size(desc)));
+  if (norm_overlap(desc, {{dx, desc->io}, {dgate, desc->io}, {dres, desc->res}},
+                   {{x, desc->io}, {gate, desc->io}, {res, desc->res}, {dy, desc->io}, {dres_out, desc->res}},
+                   {w, scale, w_res, lengths}))
+    return WTCONV_ERR_ARG;
   return with_io(desc->io, [&](auto io) {
     using IO = decltype(io);
     return with_io(desc->res, [&](auto rio) {

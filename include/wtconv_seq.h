@@ -43,9 +43,10 @@
  *     pointers, strides and channel counts suit wide loads use them.
  *   - Input rows may overlap or repeat (strides of 0 or more); rows of an
  *     output must not: token by token within a batch row, or batch rows
- *     within a token.  Outputs must not overlap inputs (those of the
- *     convolution and the scan that begin at one are refused), except that a
- *     state may be updated in place (state_out == state).
+ *     within a token.  Outputs must not overlap inputs, except that a state
+ *     may be updated in place (state_out == state).  Calls in which an output
+ *     begins where an input does are refused where threads would read what
+ *     others have written.
  *   - Workspaces hold a call's partial sums while it runs and may be reused
  *     by the next call on the same stream.
  *   - Arithmetic is fp32; the sums over a row's channels or tokens included.

@@ -1,0 +1,116 @@
+"""Refusals and sizes of the sequence operators' C entries, without a GPU: the
+addresses are made up, so nothing here may run where a call could be launched."""
+import pytest
+import torch
+
+import depthwise_convolution_wtconv_b200 as wt
+from depthwise_convolution_wtconv_b200 import _seq
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+
+ARG = 1
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return wt.load_seq()
+
+
+def P(k):
+    """Addresses far apart, one for each k."""
+    return 0x10000 + (k << 32)
+
+
+def R(k, sb=1 << 16, st=64):
+    return _seq.Rows(P(k), sb, st)
+
+
+# ------------------------------------- outputs that begin where an input does
+CAUSAL = dict(x=1, w=2, bias=3, state=4, lengths=5, y=6, state_out=7)
+CAUSAL_BACK = dict(x=1, dy=2, w=3, bias=4, state=5, lengths=6, dstate_out=7, dx=8, dw=9, dbias=10, dstate=11)
+CAUSAL_STEP = dict(x=1, w=2, bias=3, active=4, y=5, state=6)
+SCAN = dict(x=1, dt=2, a=3, b=4, c=5, d=6, z=7, dt_bias=8, state=9, lengths=10, y=11, state_out=12)
+SCAN_BACK = dict(x=1, dt=2, a=3, b=4, c=5, d=6, z=7, dt_bias=8, state=9, lengths=10, dy=11, dstate_out=12, dx=13, ddt=14, da=15, db=16,
+                 dc=17, dd=18, dz=19, ddt_bias=20, dstate=21)
+SCAN_STEP = dict(x=1, dt=2, a=3, b=4, c=5, d=6, z=7, dt_bias=8, active=9, y=10, state=11)
+NORM = dict(x=1, gate=2, w=3, res=4, scale=5, w_res=6, lengths=7, y=8, res_out=9)
+NORM_BACK = dict(x=1, gate=2, w=3, res=4, scale=5, w_res=6, lengths=7, dy=8, dres_out=9, dx=10, dgate=11, dw=12, dres=13, dscale=14,
+                 dw_res=15)
+ROWS = {"x", "y", "dy", "dx", "dt", "b", "c", "z", "ddt", "db", "dc", "dz", "gate", "res", "res_out", "dres_out", "dgate", "dres"}
+
+
+def call(lib, name, desc, places, strides={}, ws=True):
+    args = [R(k, **strides.get(m, {})) if m in ROWS else P(k) for m, k in places.items()]
+    return getattr(lib, name)(desc, *args, *([P(90), 1 << 40] if ws else []), None)
+
+
+def pairs(table, outs, ins):
+    return [(o, i) for o in outs for i in ins if o in table and i in table]
+
+
+@pytest.mark.parametrize("out,at", pairs(CAUSAL, ("y", "state_out"), ("x", "w", "bias", "lengths")) + [("y", "state")])
+def test_causal_forward_over_an_input(lib, out, at):
+    d = _seq.CausalDesc(2, 8, 64, 4, F32, 1)
+    assert call(lib, "wtconv_causal_forward", d, {**CAUSAL, out: CAUSAL[at]}, ws=False) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(CAUSAL_BACK, ("dx", "dstate"), ("x", "dy", "w", "bias", "lengths", "dstate_out")) +
+                         [("dx", "state")])
+def test_causal_backward_over_an_input(lib, out, at):
+    d = _seq.CausalDesc(2, 8, 64, 4, F32, 1)
+    assert call(lib, "wtconv_causal_backward", d, {**CAUSAL_BACK, out: CAUSAL_BACK[at]}) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(CAUSAL_STEP, ("y",), ("w", "bias", "active", "state")) +
+                         pairs(CAUSAL_STEP, ("state",), ("x", "w", "bias", "active")))
+def test_causal_step_over_an_input(lib, out, at):
+    d = _seq.CausalDesc(2, 1, 64, 4, F32, 1)
+    assert call(lib, "wtconv_causal_step", d, {**CAUSAL_STEP, out: CAUSAL_STEP[at]}, ws=False) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(SCAN, ("y", "state_out"), ("x", "dt", "a", "b", "c", "d", "z", "dt_bias", "lengths")) +
+                         [("y", "state")])
+def test_scan_forward_over_an_input(lib, out, at):
+    d = _seq.ScanDesc(2, 8, 64, 16, 1, F32, 1)
+    assert call(lib, "wtconv_scan_forward", d, {**SCAN, out: SCAN[at]}) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(SCAN_BACK, ("dx", "ddt", "db", "dc", "dz", "dstate"),
+                                         ("x", "dt", "a", "b", "c", "d", "z", "dt_bias", "lengths", "dy", "dstate_out")) +
+                         pairs(SCAN_BACK, ("dx", "ddt", "db", "dc", "dz"), ("state",)))
+def test_scan_backward_over_an_input(lib, out, at):
+    d = _seq.ScanDesc(2, 8, 64, 16, 1, F32, 1)
+    assert call(lib, "wtconv_scan_backward", d, {**SCAN_BACK, out: SCAN_BACK[at]}) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(SCAN_STEP, ("y",), ("a", "b", "c", "d", "dt_bias", "active", "state")) +
+                         pairs(SCAN_STEP, ("state",), ("x", "dt", "a", "b", "c", "d", "z", "dt_bias", "active")))
+def test_scan_step_over_an_input(lib, out, at):
+    d = _seq.ScanDesc(2, 1, 64, 16, 1, F32, 1)
+    assert call(lib, "wtconv_scan_step", d, {**SCAN_STEP, out: SCAN_STEP[at]}, ws=False) == ARG
+
+
+@pytest.mark.parametrize("name,desc,places,at", [("wtconv_causal_step", _seq.CausalDesc(2, 1, 64, 4, F32, 1), CAUSAL_STEP, "x")] +
+                         [("wtconv_scan_step", _seq.ScanDesc(2, 1, 64, 16, 1, F32, 1), SCAN_STEP, m) for m in ("x", "dt", "z")])
+def test_steps_in_place_of_other_rows(lib, name, desc, places, at):
+    """A step may write where its input lies, but not in rows that lie otherwise."""
+    assert call(lib, name, desc, {**places, "y": places[at]}, {"y": dict(sb=1 << 17)}, ws=False) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(NORM, ("y", "res_out"), ("x", "gate", "res", "w", "scale", "w_res", "lengths")))
+def test_norm_forward_over_an_input(lib, out, at):
+    """Refused: parameters, rows that lie otherwise, and rows of another type."""
+    d = _seq.NormDesc(2, 8, 64, BF16, F32, 1e-6)
+    other_type = (out == "y") != (at in ("x", "gate"))
+    for strides in [{}] if at not in ROWS or other_type else [dict(sb=1 << 17), dict(st=128)]:
+        assert call(lib, "wtconv_norm_forward", d, {**NORM, out: NORM[at]}, {out: strides}, ws=False) == ARG
+
+
+@pytest.mark.parametrize("out,at", pairs(NORM_BACK, ("dx", "dgate", "dres"), ("x", "gate", "res", "dy", "dres_out", "w", "scale", "w_res",
+                                                                              "lengths")))
+def test_norm_backward_over_an_input(lib, out, at):
+    d = _seq.NormDesc(2, 8, 64, BF16, F32, 1e-6)
+    other_type = (out == "dres") != (at in ("res", "dres_out"))
+    for strides in [{}] if at not in ROWS or other_type else [dict(sb=1 << 17), dict(st=128)]:
+        assert call(lib, "wtconv_norm_backward", d, {**NORM_BACK, out: NORM_BACK[at]}, {out: strides}) == ARG

@@ -124,3 +124,57 @@ def test_scan_decay_beyond_fp32_of_a_large_state(cuda_ok):
     s["dy"].zero_()
     s["dy"][:, -1] = 1e30
     _check_scan(s, ("y", "state", "dstate"))
+
+
+# ------------------------------------- what may share memory
+def test_steps_and_norms_where_their_inputs_lie(cuda_ok):
+    """Every value is read by the thread that writes there: with the same rows, outputs in place of inputs are the same."""
+    s = cuda(scan_case(5, 1, 72, 16, "bf16", seed=33))
+    one = {m: s[m][:, 0] for m in ("x", "dt", "b", "c", "z")}
+
+    def scan(at=None):
+        q = {m: t.clone() for m, t in one.items()}
+        held = s["state"].clone()
+        y = wt.scan_step(q["x"], q["dt"], held, s["a"], q["b"], q["c"], s["d"], q["z"], s["dt_bias"], y=at and q[at])
+        return y, held
+    want = scan()
+    for m in ("x", "dt", "z"):
+        got = scan(m)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), m
+    c = cuda(sc.causal_case(5, 1, 72, 4, "bf16", seed=34))
+    x, h1, h2 = c["x"][:, 0].clone(), c["state"].clone(), c["state"].clone()
+    want = wt.causal_step(x, h1, c["w"], c["b"])
+    assert torch.equal(wt.causal_step(x, h2, c["w"], c["b"], y=x), want) and torch.equal(h1, h2)
+    for C in (64, 4104, 8200):  # 8, 16 and 32 values a thread
+        n = cuda(sc.norm_case(3, 120, C, "f32", res="f32", ragged=True, seed=35))
+        q = {m: n[m].clone() for m in ("x", "gate", "res", "dy", "dres")}
+        args = lambda d: (d["x"], n["w"], d["gate"], d["res"], n["scale"], n["w_res"])
+        want = wt.norm_forward(*args(n), lengths=n["lengths"])
+        got = wt.norm_forward(*args(q), lengths=n["lengths"], y=q["x"], res_out=q["res"])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        back = lambda d, g: wt.norm_backward(d["x"], d["dy"], n["w"], d["gate"], d["res"], n["scale"], n["w_res"], dres=d["dres"],
+                                             lengths=n["lengths"], grads=g)
+        q = {m: n[m].clone() for m in q}
+        want = back(n, None)
+        got = back(q, dict(want, dx=q["x"], dgate=q["gate"], dres=q["dres"], dw=want["dw"].clone(), dscale=want["dscale"].clone(),
+                           dw_res=want["dw_res"].clone()))
+        for m in want:
+            assert torch.equal(got[m], want[m]), m
+
+
+@pytest.mark.parametrize("T", [20, 1000])
+def test_gradient_of_the_state_in_place_of_the_state(cuda_ok, T):
+    s = cuda(scan_case(2, T, 64, 16, "f32", seed=36))
+    call = lambda state, g: wt.scan_backward(s["x"], s["dt"], s["a"], s["b"], s["c"], s["dy"], s["d"], s["z"], s["dt_bias"], state=state,
+                                             dstate=s["dstate"], grads=g)
+    want = call(s["state"], None)
+    held = s["state"].clone()
+    got = call(held, {m: held if m == "dstate" else torch.empty_like(t) for m, t in want.items()})
+    for m in want:
+        assert torch.equal(got[m], want[m]), m
+    c = cuda(sc.causal_case(2, T, 64, 4, "f32", seed=37))
+    call = lambda state, g: wt.causal_backward(c["x"], c["dy"], c["w"], c["b"], state=state, dstate=c["dstate"], grads=g)
+    dx, want = call(c["state"], None)
+    held = c["state"].clone()
+    dx2, got = call(held, {m: held if m == "dstate" else torch.empty_like(t) for m, t in want.items()})
+    assert torch.equal(dx, dx2) and all(torch.equal(got[m], want[m]) for m in want)
