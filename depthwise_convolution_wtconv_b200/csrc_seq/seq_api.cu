@@ -18,6 +18,7 @@ namespace {
 constexpr long long MAX_ELEMENTS = 1ll << 56;  // byte offsets stay within 64 bits
 constexpr long long MAX_TOKEN_STRIDE = INT_MAX;  // kernels hold it in 32 bits
 constexpr int MAX_TOKENS = 1 << 30;  // of a row: token counts and tiles stay within 32 bits
+constexpr int MAX_ROW = INT_MAX - 4095;  // elements of a token's row: kernels hold a channel, rounded up to a block's, in 32 bits
 constexpr int SMS = 148;
 
 size_t elt(wtconv_dtype t) { return t == WTCONV_F32 ? 4 : 2; }
@@ -92,7 +93,7 @@ bool grid_ok(long long blocks) { return blocks <= INT_MAX; }
 // ------------------------------------------------------ causal convolution
 wtconv_status check_causal(const wtconv_causal_desc* d) {
   if (!d || d->B <= 0 || d->T <= 0 || d->T > MAX_TOKENS || d->C <= 0 || d->k <= 0 || !dtype_ok(d->io)) return WTCONV_ERR_ARG;
-  if ((long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
+  if (d->C > MAX_ROW || (long long)d->B * d->T > MAX_ELEMENTS / d->C) return WTCONV_ERR_ARG;
   return d->k > WTCONV_CAUSAL_MAX_K ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
 }
 
@@ -172,11 +173,20 @@ wtconv_status causal_step(const CausalArgs<IO>& a, int k, const int* active, cud
 }
 
 // -------------------------------------------------------------------- scan
+// A group's channels and states as the kernels read them: rounded up to 16
+// bytes and to four, by copies where that is more than there are.
+long long scan_group(const wtconv_scan_desc* d) {
+  const long long e = 16 / elt(d->io);
+  return ceil_div(d->C / d->G, e) * e;
+}
+int scan_states(const wtconv_scan_desc* d) { return (d->N + 3) / 4 * 4; }
+
 wtconv_status check_scan(const wtconv_scan_desc* d) {
   if (!d || d->B <= 0 || d->T <= 0 || d->T > MAX_TOKENS || d->C <= 0 || d->N <= 0 || d->G <= 0 || d->C % d->G || !dtype_ok(d->io))
     return WTCONV_ERR_ARG;
-  if ((long long)d->B * d->T > MAX_ELEMENTS / d->C / 64) return WTCONV_ERR_ARG;
-  return d->N > WTCONV_SCAN_MAX_N ? WTCONV_ERR_UNSUPPORTED : WTCONV_OK;
+  if (d->N > WTCONV_SCAN_MAX_N) return WTCONV_ERR_UNSUPPORTED;
+  if (d->G * scan_group(d) > MAX_ROW || (long long)d->G * scan_states(d) > MAX_ROW) return WTCONV_ERR_ARG;
+  return (long long)d->B * d->T > MAX_ELEMENTS / d->C / 64 ? WTCONV_ERR_ARG : WTCONV_OK;
 }
 
 int scan_blocks(const wtconv_scan_desc* d) { return (int)ceil_div(d->C / d->G, 32); }
@@ -193,14 +203,6 @@ void scan_plan(const wtconv_scan_desc* d, int* chunks, int* chunk_tiles) {
   *chunk_tiles = (int)ceil_div(tiles, n);
   *chunks = (int)ceil_div(tiles, *chunk_tiles);
 }
-
-// A group's channels and states as the kernels read them: rounded up to 16
-// bytes and to four, by copies where that is more than there are.
-int scan_group(const wtconv_scan_desc* d) {
-  const int e = (int)(16 / elt(d->io));
-  return (int)ceil_div(d->C / d->G, e) * e;
-}
-int scan_states(const wtconv_scan_desc* d) { return (d->N + 3) / 4 * 4; }
 
 struct ScanWs {  // bytes into the workspace, each part on 16
   size_t ends, sums, grad_ends, pads, ckpt, part_b, part_c, part_a, part_d, part_bias, end;

@@ -71,7 +71,8 @@ extern "C" {
 
 /* Rows of an activation: channel c of token t of batch row b is
  * data[b * batch_stride + t * token_stride + c], strides in elements (the
- * token stride at most 2^31 - 1). */
+ * token stride at most 2^31 - 1), at most 2^31 - 4096 elements a token (of the
+ * scan's, with each group's rounded up to 16 bytes and to four states). */
 typedef struct {
   void* data;
   long long batch_stride, token_stride;

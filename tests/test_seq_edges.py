@@ -114,3 +114,24 @@ def test_norm_backward_over_an_input(lib, out, at):
     other_type = (out == "dres") != (at in ("res", "dres_out"))
     for strides in [{}] if at not in ROWS or other_type else [dict(sb=1 << 17), dict(st=128)]:
         assert call(lib, "wtconv_norm_backward", d, {**NORM_BACK, out: NORM_BACK[at]}, {out: strides}) == ARG
+
+
+# --------------------------------------------- rows beyond 32-bit channels
+@pytest.mark.parametrize("C,G,N", [(2 ** 31 - 1, 1, 1), (2 ** 28, 2 ** 28, 4), (2 ** 25, 2 ** 25, 64), (2 ** 25, 2 ** 25, 61)])
+def test_scan_rows_of_too_many_elements(lib, C, G, N):
+    """Channels (rounded up in each group) and states of a token have to fit 32 bits, also where they are copied to
+    rounded-up rows."""
+    places = {m: k for m, k in SCAN.items()}
+    wide = {m: dict(sb=1 << 40, st=(1 << 31) - 1) for m in ROWS}
+    for T in (1, 2):
+        d = _seq.ScanDesc(1, T, C, N, G, BF16, 1)
+        assert call(lib, "wtconv_scan_forward", d, places, wide) == ARG
+        assert lib.wtconv_scan_workspace_size(d, 0) == 0 and lib.wtconv_scan_workspace_size(d, 1) == 0
+
+
+def test_causal_rows_of_too_many_elements(lib):
+    d = _seq.CausalDesc(1, 1, 2 ** 31 - 1, 4, BF16, 1)
+    assert call(lib, "wtconv_causal_forward", d, CAUSAL, ws=False) == ARG
+    assert lib.wtconv_causal_workspace_size(d) == 0
+    assert lib.wtconv_causal_workspace_size(_seq.CausalDesc(1, 1, 2 ** 31 - 4096, 4, BF16, 1)) > 0
+    assert lib.wtconv_scan_workspace_size(_seq.ScanDesc(1, 1, 2 ** 31 - 4096, 4, 1, BF16, 1), 1) > 0
