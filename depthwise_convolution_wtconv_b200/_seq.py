@@ -13,9 +13,14 @@ import ctypes
 import struct
 
 import torch
-from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _current_device
 
 from ._lib import BF16, F32, _check, load
+
+# The current stream's address and the current device's index, without the
+# objects around them.  A torch built without CUDA has neither; no call gets as
+# far there, since its tensors are refused before.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 # every symbol include/wtconv_seq.h declares
 EXPORTS_SEQ = ("wtconv_causal_forward", "wtconv_causal_backward", "wtconv_causal_step", "wtconv_causal_workspace_size",

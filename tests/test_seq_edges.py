@@ -1,5 +1,9 @@
 """Refusals and sizes of the sequence operators' C entries, without a GPU: the
 addresses are made up, so nothing here may run where a call could be launched."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -135,3 +139,29 @@ def test_causal_rows_of_too_many_elements(lib):
     assert lib.wtconv_causal_workspace_size(d) == 0
     assert lib.wtconv_causal_workspace_size(_seq.CausalDesc(1, 1, 2 ** 31 - 4096, 4, BF16, 1)) > 0
     assert lib.wtconv_scan_workspace_size(_seq.ScanDesc(1, 1, 2 ** 31 - 4096, 4, 1, BF16, 1), 1) > 0
+
+
+# ------------------------------------------------- torch without CUDA
+def test_package_without_the_bindings_of_cuda():
+    """A torch built without CUDA lacks the calls for the current stream and device: the package still imports, what needs
+    no GPU still answers, and tensors are refused as ever."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import depthwise_convolution_wtconv_b200 as wt
+from depthwise_convolution_wtconv_b200 import _seq
+d = wt.make_desc(2, 8, 16, 16, 5, 2, "f32")
+assert wt.kernel_launches(d, 3) > 0 and wt.workspace_size(d, 3) >= 0
+assert wt.load_seq().wtconv_causal_workspace_size(_seq.CausalDesc(2, 8, 64, 4, 0, 1)) > 0
+try:
+    wt.causal_forward(torch.zeros(1, 2, 8), torch.zeros(8, 4))
+except TypeError as e:
+    assert "CUDA tensor" in str(e)
+else:
+    raise AssertionError("not refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
