@@ -452,8 +452,24 @@ int norm_blocks(const wtconv_norm_desc* d, int threads, int per_sm) {
   const long long most = (long long)SMS * std::max(1, std::min(16, per_sm / threads));
   return (int)std::min<long long>((long long)d->B * d->T, most);
 }
-// The most blocks of the gradients, whatever the variant: of one warp.
-int norm_grad_blocks(const wtconv_norm_desc* d) { return norm_blocks(d, 32, NORM_GRAD_THREADS); }
+// Chunks of V channels a thread: 8 values while 512 threads hold the row, then
+// 16 and 32.  Threads of a row.
+int norm_threads(int C, int V, int nv) { return (int)ceil_div(ceil_div(ceil_div(C, V), nv), 32) * 32; }
+int norm_chunks(int C, int V) {
+  int nv = 8 / V;
+  while (nv < 32 / V && norm_threads(C, V, nv) > 512) nv *= 2;
+  return nv;
+}
+int norm_threads(int C, int V) { return norm_threads(C, V, norm_chunks(C, V)); }
+// Channels of a chunk of neighbours, 16 bytes of them; of a chunk at odd rows.
+constexpr int norm_wide(size_t e) { return (int)(16 / e); }
+constexpr int NORM_ODD = 8;
+// The most blocks of the gradients: the size of the workspace does not depend
+// on whether the rows suit wide loads.
+int norm_grad_blocks(const wtconv_norm_desc* d) {
+  const int threads = std::min(norm_threads(d->C, NORM_ODD), norm_threads(d->C, norm_wide(elt(d->io))));
+  return norm_blocks(d, threads, NORM_GRAD_THREADS);
+}
 
 template <typename IO, typename RES>
 NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, const wtconv_rows* gate, const float* w,
@@ -473,21 +489,17 @@ NormArgs<IO, RES> norm_args(const wtconv_norm_desc* d, const wtconv_rows* x, con
   return a;
 }
 
-// Threads and chunks of a row: 8 values a thread while 512 threads hold the
-// row, then 16 and 32.  f gets V, NV and the threads.
+// Calls f with V, NV, whether chunks are neighbouring channels, and the threads.
 template <int V, typename F> wtconv_status norm_shape(int C, F f) {
-  const int chunks = (int)ceil_div(C, V);
   constexpr int N1 = 8 / V, N2 = 16 / V, N3 = 32 / V;
-  auto threads = [&](int nv) { return (int)ceil_div(ceil_div(chunks, nv), 32) * 32; };
-  if (threads(N1) <= 512) return f(Int<V>(), Int<N1>(), threads(N1));
-  if (threads(N2) <= 512) return f(Int<V>(), Int<N2>(), threads(N2));
-  return f(Int<V>(), Int<N3>(), threads(N3));
+  const int nv = norm_chunks(C, V), threads = norm_threads(C, V);
+  if (nv == N1) return f(Int<V>(), Int<N1>(), threads);
+  if (nv == N2) return f(Int<V>(), Int<N2>(), threads);
+  return f(Int<V>(), Int<N3>(), threads);
 }
-
-// ... and whether chunks are neighbouring channels, 16 bytes of them.
 template <typename IO, typename F> wtconv_status norm_variant(int C, bool vec, F f) {
-  if (vec) return norm_shape<sizeof(IO) == 2 ? 8 : 4>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::true_type(), t); });
-  return norm_shape<8>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::false_type(), t); });
+  if (vec) return norm_shape<norm_wide(sizeof(IO))>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::true_type(), t); });
+  return norm_shape<NORM_ODD>(C, [&](auto v, auto nv, int t) { return f(v, nv, std::false_type(), t); });
 }
 
 // Calls f with the I/O type (and the type of the residual).
@@ -750,7 +762,7 @@ wtconv_status wtconv_norm_forward(const wtconv_norm_desc* desc, const wtconv_row
       NormArgs<IO, RES> a = norm_args<IO, RES>(desc, x, gate, w, res, scale, w_res, lengths);
       a.y = rows_of<IO>(y, T);
       a.res_out = rows_of<RES>(res_out, T);
-      constexpr int V = sizeof(IO) == 2 ? 8 : 4;
+      constexpr int V = norm_wide(sizeof(IO));
       const bool vec = C % V == 0 && wide(x, V, sizeof(IO), B, T) && wide(gate, V, sizeof(IO), B, T) &&
                        wide(y, V, sizeof(IO), B, T) && wide(res, V, sizeof(RES), B, T) &&
                        wide(res_out, V, sizeof(RES), B, T);
@@ -807,7 +819,7 @@ wtconv_status wtconv_norm_backward(const wtconv_norm_desc* desc, const wtconv_ro
       a.dgate = rows_of<IO>(dgate, T);
       a.dres = rows_of<RES>(dres, T);
       a.part = static_cast<float*>(ws);
-      constexpr int V = sizeof(IO) == 2 ? 8 : 4;
+      constexpr int V = norm_wide(sizeof(IO));
       const size_t e = sizeof(IO), re = sizeof(RES);
       const bool vec = C % V == 0 && wide(x, V, e, B, T) && wide(gate, V, e, B, T) && wide(dy, V, e, B, T) &&
                        wide(dx, V, e, B, T) && wide(dgate, V, e, B, T) && wide(res, V, re, B, T) &&

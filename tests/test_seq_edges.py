@@ -165,3 +165,15 @@ else:
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+# ------------------------------------------------- the norm's workspace
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("C", [1, 64, 250, 2048, 2049, 4096, 4097, 5120, 8192, 8200, 16383, 16384])
+def test_norm_workspace_is_what_its_blocks_leave(lib, C, io):
+    """Three sums a channel of every block; a block is the threads that hold a row, 512 threads on each of 148 SMs."""
+    values = next(v for v in (8, 16, 32) if -(-C // v) <= 512)
+    threads = -(-C // values // 32) * 32
+    for B, T in ((1, 1), (3, 7), (64, 1024)):
+        blocks = min(B * T, 148 * max(1, min(16, 512 // threads)))
+        assert lib.wtconv_norm_workspace_size(_seq.NormDesc(B, T, C, io, F32, 1e-6)) == (blocks * 3 * C * 4 + 15) // 16 * 16
