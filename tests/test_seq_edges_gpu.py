@@ -178,3 +178,94 @@ def test_gradient_of_the_state_in_place_of_the_state(cuda_ok, T):
     held = c["state"].clone()
     dx2, got = call(held, {m: held if m == "dstate" else torch.empty_like(t) for m, t in want.items()})
     assert torch.equal(dx, dx2) and all(torch.equal(got[m], want[m]) for m in want)
+
+
+# ------------------------------------- every variant against the oracle
+# Norms: rows of 8, 16 and 32 values a thread (up to 4096, 8192 and 16384 channels), wide and odd, more rows than blocks, so
+# that blocks go on from row to row and the parameters' gradients are sums over rows within a block and over blocks.
+PARTS = [dict(), dict(gate=False, w=False), dict(w_res=False, scale=False)]
+NORM = [dict(B=2, T=(T if rows else 1), C=C, io=io, res=None if alone else res, ragged=bool(rows and i % 2), **({} if alone else PARTS[i % 3]))
+        for i, (C, T) in enumerate([(2048, 170), (2047, 170), (4097, 80), (5120, 80), (5119, 80), (8192, 80), (8201, 80), (16384, 75),
+                                    (16383, 75)])
+        for io, res, alone, rows in [("f32", "f32", False, True), ("bf16", "f32", False, True), ("bf16", "bf16", True, True),
+                                     ("f32", "bf16", False, False), ("bf16", "bf16", False, False)]]
+
+
+def _name(c):
+    return "-".join(f"{k}{v}" for k, v in c.items())
+
+
+@pytest.mark.parametrize("case", NORM, ids=_name)
+def test_norm_of_every_width(cuda_ok, case):
+    """The longest chain behind a value: 32 values a thread and the sums over the block (24 + C / 8 covers both), twice on the
+    way back; for the parameters also the rows of a block and the blocks, at most B T / 8 in a row."""
+    s = sc.norm_case(**case, seed=41)
+    d = cuda(s)
+    args = (d["w"], d["gate"], d["res"], d["scale"], d["w_res"])
+    y, res = wt.norm_forward(d["x"], *args, lengths=d["lengths"])
+    g = wt.norm_backward(d["x"], d["dy"], *args, dres=d["dres"], lengths=d["lengths"])
+    want, size = sc.norm_oracle(s, True), sc.norm_oracle(s, True, mag=True)
+    ops = 24 + case["C"] / 8
+    check(y, want["y"], size["y"], ops, "y")
+    check(res, want["res"], size["res"], ops, "res")
+    given = dict(dgate=s["gate"], dw=s["w"], dres=s["res"], dscale=s["scale"], dw_res=s["w_res"])
+    for m in ("dx", "dgate", "dw", "dres", "dscale", "dw_res"):
+        check(g[m], None if m in given and given[m] is None else want.get(m), size.get(m), 2 * ops + 4 + case["B"] * case["T"] / 8, m)
+
+
+def _check_causal(s, k, strip):
+    d = cuda(s)
+    y, state = wt.causal_forward(d["x"], d["w"], d["b"], state=d["state"], lengths=d["lengths"])
+    dx, g = wt.causal_backward(d["x"], d["dy"], d["w"], d["b"], state=d["state"], lengths=d["lengths"], dstate=d["dstate"])
+    want, size = sc.causal_oracle(s, grads=True), sc.causal_oracle(s, grads=True, mag=True)
+    check(y, want["y"], size["y"], k + 8, "y")
+    assert torch.equal(state.double().cpu(), torch.from_numpy(want["state"]))
+    check(dx, want["dx"], size["dx"], 2 * k + 10, "dx")
+    check(g["dstate"], want["dstate"], size["dstate"], 2 * k + 10, "dstate")
+    # in a row: a strip's tokens, the 8 strips of a block, a slice of the blocks and the slices
+    ops = k + 10 + strip + 8 + 32 + 32
+    check(g["dw"], want["dw"], size["dw"], ops, "dw")
+    check(g["db"], want["db"], size["db"], ops, "db")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("k", range(1, 9))
+def test_causal_by_two_channels(cuda_ok, k, io):
+    """Channel counts that are even and no multiple of four."""
+    _check_causal(sc.causal_case(4, 37, 66, k, io, ragged=True, seed=42), k, 16)
+
+
+@pytest.mark.parametrize("T,C,k,io", [(2433, 4096, 5, "bf16"), (2433, 4096, 7, "f32"), (2433, 4098, 3, "bf16"), (1217, 4096, 3, "f32"),
+                                      (1217, 4099, 4, "bf16")])
+def test_causal_in_long_strips(cuda_ok, T, C, k, io):
+    """Enough threads for strips of 64 tokens (gradients 128), and of 32 (64): T one past a strip, rows that end within
+    one and one past one, taps that do not divide it, states in and out."""
+    s = sc.causal_case(3, T, C, k, io, seed=43)
+    s["lengths"] = torch.tensor([T, T - 255, T // 3 + 1], dtype=torch.int32)
+    s["x"], s["dy"] = sc.poison(s["x"], s["lengths"]), sc.poison(s["dy"], s["lengths"])
+    _check_causal(s, k, 128)
+
+
+@pytest.mark.parametrize("T", [16, 40, 700])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_tokens_that_do_not_move_a_state(cuda_ok, T, io):
+    """A step of zero leaves a state as it is, to the bit, and so do the tokens behind a length, which are steps of zero in
+    the kernel: within a tile of 16 tokens, behind it, and over chunks."""
+    s = scan_case(4, T, 40, 16, io, bias=False, seed=44)
+    s["dt"] = (0.05 * s["dt"].abs()).to(s["dt"].dtype)
+    n = torch.tensor([1, 5, 15, 0], dtype=torch.int32) + (T - 16)
+    live = (torch.arange(T) < n[:, None])[..., None]
+    d = cuda(dict(s, dt=torch.where(live, s["dt"], 0), dy=torch.where(live, s["dy"], 0)))
+    args = lambda q: (q["x"], q["dt"], q["a"], q["b"], q["c"])
+    run = lambda q, n: (wt.scan_forward(*args(q), q["d"], q["z"], softplus=False, state=q["state"], lengths=n),
+                        wt.scan_backward(*args(q), q["dy"], q["d"], q["z"], softplus=False, state=q["state"], lengths=n,
+                                         dstate=q["dstate"]))
+    cut = {m: sc.poison(d[m], n) if m in ("x", "dt", "b", "c", "z", "dy") else d[m] for m in d}
+    (y, state), g = run(d, None)
+    (y2, state2), g2 = run(cut, n.cuda())
+    live = live.cuda()
+    assert torch.equal(state, state2) and torch.equal(torch.where(live, y, 0), y2)
+    assert torch.equal(g["dstate"], g2["dstate"]) and torch.equal(torch.where(live, g["dx"], 0), g2["dx"])
+    still = dict(d, dt=torch.zeros_like(d["dt"]), dy=torch.zeros_like(d["dy"]))
+    (_, state), g = run(still, None)
+    assert torch.equal(state, d["state"]) and torch.equal(g["dstate"], d["dstate"])
