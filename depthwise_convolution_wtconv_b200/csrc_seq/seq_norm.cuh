@@ -7,9 +7,14 @@
 // thread) the next row's inputs are on their way while a row is worked on.
 //
 // Memory is the floor.  8x2048x2048 bf16 with an fp32 residual and all parts:
-// forward 88 us (5.3 TB/s, 82% of the floor), gradients 178 us (4.1 TB/s, 63%;
+// forward 82 us (5.7 TB/s, 88% of the floor), gradients 177 us (4.2 TB/s, 64%;
 // 126 registers leave 16 warps an SM).  One row a block at a time, loads only
 // when needed, took 141 and 487 us.
+// Rows that begin at odd addresses go by single channels: 8x2048x2047 takes 177
+// and 522 us (the gradients spill 72 bytes a thread).  Rows of more than 4096
+// channels have 16 or 32 values a thread, loads only when needed, and spilled
+// gradients (0.5 to 2.5 KB): 8x800x5120 203 and 530 us, floors 70 and 110;
+// 8x256x16384 193 and 802 us, floors 72 and 113.
 #pragma once
 
 #include "seq_common.cuh"
@@ -146,7 +151,8 @@ template <typename IO, int V, int NV, bool WIDE> struct RowIn {
 };
 
 // NT: the most threads of a block.  Rows of 8 values a thread run at 64
-// registers, which fills an SM with 1024 threads.
+// registers, which fills an SM with 1024 threads (8 values of fp32 with an fp32
+// residual spill 16 bytes for that, odd rows 48 to 56).
 template <typename IO, typename RES, int V, int NV, bool WIDE, int NT>
 __global__ void __launch_bounds__(NT, V * NV <= 8 ? NORM_THREADS / NT : 1) norm_forward_kernel(NormArgs<IO, RES> a) {
   constexpr bool AHEAD = V * NV <= 8;

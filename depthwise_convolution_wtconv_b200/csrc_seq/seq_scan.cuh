@@ -15,7 +15,7 @@
 // Bound by instructions: 610 a warp and tile, 274 of them B (16 values: per
 // value an exponential, half a packed multiply-add each for its argument, the
 // input and the sum, a multiply-add for h), the rest A, C and the copies, once
-// for all states.  8x2048x2048 bf16 with 16 states: 287 us, where its 537 M
+// for all states.  8x2048x2048 bf16 with 16 states: 286 us, where its 537 M
 // exponentials alone take 115 us and its bytes 41 us.  Four states a warp: four
 // chains keep the multiply-adds busy, and the warps together halve the share
 // of A and C; delta of a whole tile in registers instead took 315 us.
@@ -591,10 +591,11 @@ __global__ void __launch_bounds__(W * 32, W >= 16 ? 1 : 20 / W) scan_forward_ker
 // j ^ (l & 3): neighbours that exchange two registers each complete one of the
 // two states.  Only the quarter that remains after two such turns is summed by
 // halving the values and the lanes that they lie on.
-// 8x1024x2048 bf16, 16 states: 653 us with the pass that keeps the states (128
+// 8x1024x2048 bf16, 16 states: 652 us with the pass that keeps the states (128
 // us) and the sums (25 us); 2200 instructions a warp and tile at 0.45 a clock,
-// 128 registers.  Selecting in every turn, as for 32 values over 32 lanes,
-// cost two instructions more a value.
+// 128 registers, of which 80 to 124 bytes a thread are spilled (448 in blocks of
+// one warp).  fp32: 853 us.  Selecting in every turn, as for 32 values over 32
+// lanes, cost two instructions more a value.
 template <typename IO> struct ScanGradSmem {
   float *de, *dx, *dp;          // [T/4][32] float4: delta, delta x, dp
   float* y;                     // [3][W][T/4][32] float4: sums over a warp's states of c h, e a k, e b
@@ -931,9 +932,9 @@ template <typename IO> __global__ void __launch_bounds__(256) scan_sums_kernel(c
 // One token of every row: four threads share a channel's states and join their
 // sums over the four.  With VEC, four states at a time: the state, 8 bytes a
 // state of traffic where everything else is less than one, goes in 16-byte
-// accesses, whole sectors of a row at once.  64x4096 bf16 with 16 states: 34
-// MB of state in 10 us, less than the call from Python takes (state by state:
-// 34 us).
+// accesses, whole sectors of a row at once.  64x4096 bf16 with 16 states, 34
+// MB of state: 12 us where three states take turns, which the L2 nearly holds,
+// 18 us with states from memory (floor 5.7); the call from Python takes 14.
 // Blocks take a column of 32 channels through every gridDim.y-th row, so that
 // what does not depend on the row is found once.
 template <typename IO, bool VEC>
