@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 
 # ------------------------------------------------------------------ causal
-# strips are 32 tokens, gradient blocks 256; vectors 8, 4 or 1 channels
+# strips are 16 tokens at these sizes, gradient blocks 128; vectors 4, 2 or 1 channels (longer strips: test_seq_edges_gpu.py)
 CAUSAL = [
     dict(B=1, T=1, C=8, k=4, io="f32"),
     dict(B=2, T=2, C=16, k=4, io="bf16"),                      # shorter than the taps
@@ -186,11 +186,11 @@ NORM = [
     dict(B=2, T=3, C=7, io="bf16", res="bf16"),
     dict(B=3, T=5, C=64, io="bf16", res="f32", ragged=True),
     dict(B=1, T=4, C=2048, io="bf16", res="f32"),
-    dict(B=2, T=2, C=2056, io="bf16", res="bf16"),              # past one chunk a thread
+    dict(B=2, T=2, C=2056, io="bf16", res="bf16"),              # one chunk a thread, one thread in the last warp
     dict(B=1, T=3, C=8200, io="f32", res="f32"),
     dict(B=1, T=2, C=16384, io="bf16", res="f32"),              # the longest row
     dict(B=1, T=2, C=16383, io="bf16", res="bf16"),             # the longest odd row
-    dict(B=2, T=350, C=40, io="f32", res="bf16", ragged=True),   # more rows than blocks in the gradient
+    dict(B=2, T=350, C=40, io="f32", res="bf16", ragged=True),   # many rows, one a block (more: test_seq_edges_gpu.py)
     dict(B=2, T=3, C=100, io="f32", gate=False),
     dict(B=2, T=3, C=100, io="bf16", w=False),
     dict(B=2, T=3, C=100, io="bf16", res="f32", gate=False, w=False),
