@@ -51,7 +51,8 @@
  *     by the next call on the same stream.
  *   - Arithmetic is fp32; the sums over a row's channels or tokens included.
  *   - WTCONV_ERR_ARG: null or negative arguments, a descriptor out of range,
- *     overlapping output rows; WTCONV_ERR_ALIGN: a pointer not aligned to its
+ *     overlapping output rows, an output where an input begins (as above);
+ *     WTCONV_ERR_ALIGN: a pointer not aligned to its
  *     elements (workspace: 16 bytes); WTCONV_ERR_WORKSPACE: workspace too
  *     small; WTCONV_ERR_UNSUPPORTED: k > 8, N > 64 or, for the norm, rows of
  *     more channels than one thread block holds (WTCONV_NORM_MAX_C).
